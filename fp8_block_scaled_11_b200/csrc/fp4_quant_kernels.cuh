@@ -1,0 +1,168 @@
+// fp4_quant_kernels.cuh -- microscaled 4-bit quantisation along the columns or
+// (transposed) along the rows, and back.  The scale rule and the layouts are in
+// mx4.cuh.  Memory-bound: every input is read once with 16-byte loads.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include "ptx.cuh"
+#include "mx4.cuh"
+#include "quant_kernels.cuh"
+
+namespace fp8bs {
+
+// The four scale bytes of a 128-column chunk from the byte of each of its four
+// groups, held by lanes 0, 4, 8, 12 of a half-warp; valid in its lane 0.
+__device__ __forceinline__ uint32_t sf_gather_word(uint32_t byte, int lane)
+{
+    const int base = lane & 16;
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= __shfl_sync(0xffffffffu, byte, base + 4 * i) << (8 * i);
+    return w;
+}
+
+// Largest magnitude over the four lanes that share a group of 32 values.
+__device__ __forceinline__ float group32_absmax(const float (&f)[8])
+{
+    float m = absmax8(f);
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+
+// --------------------------------------------------------------------------
+// Groups along the columns.  A CTA owns a scale tile's 128 rows x 128 columns;
+// half-warp h of 16 takes rows h, h + 16 (mod 32) of each of the four 32-row
+// quarters, whose scale words are adjacent in the tile (one 16-byte store).
+// --------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(256) fp4_quant_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
+                                                             int64_t ldx, uint8_t* __restrict__ q, int64_t ldq,
+                                                             uint8_t* __restrict__ sf, int64_t kcs)
+{
+    const int lane = threadIdx.x & 31;
+    const int hw = threadIdx.x >> 4;
+    const int64_t rb = blockIdx.x / kcs, kc = blockIdx.x - rb * kcs;
+    const int64_t c = kc * 128 + (threadIdx.x & 15) * 8;
+    const bool col_ok = c < cols;           // cols % 32 == 0: a group is all in or all out
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t r0 = rb * 128 + hw + 16 * i;
+        Vec8<T> v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (col_ok && r0 + 32 * j < rows) v[j].load(x + (r0 + 32 * j) * ldx + c);
+            else v[j].zero();
+        }
+        uint32_t word[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float f[8];
+            v[j].get(f);
+            const uint32_t byte = mx4_scale_byte(group32_absmax(f));
+            const uint32_t codes = mx4_pack8(f, mx4_inv_scale(byte));
+            if (col_ok && r0 + 32 * j < rows) *reinterpret_cast<uint32_t*>(q + (r0 + 32 * j) * ldq + (c >> 1)) = codes;
+            word[j] = sf_gather_word(col_ok ? byte : 127u, lane);
+        }
+        // rows past the last one keep their bytes
+        if ((lane & 15) == 0) {
+            uint8_t* dst = sf + sf_word_offset(r0, kc, kcs);
+            if (r0 + 96 < rows) {
+                *reinterpret_cast<uint4*>(dst) = make_uint4(word[0], word[1], word[2], word[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (r0 + 32 * j < rows) *reinterpret_cast<uint32_t*>(dst + 4 * j) = word[j];
+            }
+        }
+    }
+}
+
+// --------------------------------------------------------------------------
+// Groups along the rows; the transposed codes and their scale tiles are written
+// (row c of the output is column c of x).  A CTA owns 128 rows x 128 columns of
+// x, as 8 x 8 blocks: warp (wr, wc) covers 32 rows, i.e. one group, of 64
+// columns.
+// --------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(256) fp4_quant_cols_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
+                                                             int64_t ldx, uint8_t* __restrict__ q, int64_t ldq,
+                                                             uint8_t* __restrict__ sf, int64_t kcs, int64_t tiles_c)
+{
+    __shared__ __align__(16) uint8_t s_sf[kSfTileBytes];
+    const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
+    int strip, group, wr, wc;
+    qblock_coords(strip, group, wr, wc);
+    const int64_t r0 = tr * 128 + group * 8;
+    const int64_t c0 = tc * 128 + strip * 8;
+    const bool ok = r0 < rows && c0 < cols;     // rows % 32 == 0, cols % 16 == 0
+    Block8x8<T> b;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (ok) b.row[i].load(x + (r0 + i) * ldx + c0);
+        else b.row[i].zero();
+    }
+    float m[8];
+    b.col_absmax(m);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 8));
+        m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t byte = mx4_scale_byte(m[j]);
+        const float s = mx4_inv_scale(byte);
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float g[8];
+            b.row[i].get(g);
+            f[i] = g[j];
+        }
+        const uint32_t codes = mx4_pack8(f, s);
+        if (ok) *reinterpret_cast<uint32_t*>(q + (c0 + j) * ldq + (r0 >> 1)) = codes;
+        // the tile's byte of output row 8 strip + j, group wr (rows past x's last: a scale of one)
+        const int row = strip * 8 + j;
+        if ((threadIdx.x & 31) < 8) s_sf[(row & 31) * 16 + (row >> 5) * 4 + wr] = (uint8_t)(r0 < rows ? byte : 127u);
+    }
+    __syncthreads();
+    if (threadIdx.x < 128) {
+        const int64_t row = tc * 128 + threadIdx.x;
+        const int at = (threadIdx.x & 31) * 16 + (threadIdx.x >> 5) * 4;
+        if (row < cols)
+            *reinterpret_cast<uint32_t*>(sf + (tc * kcs + tr) * (int64_t)kSfTileBytes + at) =
+                *reinterpret_cast<const uint32_t*>(s_sf + at);
+    }
+}
+
+// --------------------------------------------------------------------------
+// Codes and scale tiles -> values (bf16 or fp32): exact, except that a value
+// outside the output type's range rounds as the type does.
+// --------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(256) fp4_dequant_kernel(const uint8_t* __restrict__ q, int64_t ldq,
+                                                          const uint8_t* __restrict__ sf, int64_t rows, int64_t cols,
+                                                          int64_t kcs, T* __restrict__ out, int64_t ldo)
+{
+    const int64_t g = cols >> 5;                  // groups per row
+    const int64_t total = rows * g * 4;           // eight values each
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t r = i / (g * 4);
+        const int64_t v = i - r * (g * 4);        // eighth of the row
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(q + r * ldq + v * 4);
+        const uint32_t byte = sf[sf_word_offset(r, v >> 4, kcs) + ((v >> 2) & 3)];
+        float f[8];
+        mx4_unpack8(w, mx4_scale_value(byte), f);
+        T* dst = out + r * ldo + v * 8;
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4*>(dst) = make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]),
+                                                        cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7]));
+        } else {
+            *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<float4*>(dst + 4) = make_float4(f[4], f[5], f[6], f[7]);
+        }
+    }
+}
+
+}  // namespace fp8bs

@@ -4,6 +4,8 @@
 // unit, so the error flag is a plain __device__ variable).  The GEMM runs on
 // single CTAs (gemm_kernel.cuh) or CTA pairs (gemm_pair_kernel.cuh), the
 // power-of-two block recipes on the block-scaled MMA kernel (gemm_bs_kernel.cuh).
+// The RMS norm's and the 4-bit entry points are in norm_fp4_entry.cuh, included
+// at the end.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -20,6 +22,9 @@
 #include "gemm_pair_kernel.cuh"
 #include "gemm_bs_kernel.cuh"
 #include "splitk_reduce.cuh"
+#include "norm_kernels.cuh"
+#include "fp4_quant_kernels.cuh"
+#include "gemm_fp4_kernel.cuh"
 
 using namespace fp8bs;
 
@@ -43,6 +48,7 @@ struct DeviceInfo {
     std::atomic<bool> tile_attr_set[16]{};   // per tile kernel kind (+8: power-of-two scale rule)
     std::atomic<int> tile_blocks[16]{};
     std::atomic<int> pair_clusters[8]{};     // co-resident CTA pairs, per pair-kernel instantiation
+    std::atomic<bool> fp4_attr_set[5]{};     // 4-bit product, per tile width
 };
 
 DeviceInfo g_dev[kMaxDevices];
@@ -1059,3 +1065,5 @@ extern "C" fp8bs_status fp8_quant_tensor_noalloc(const void* x, fp8bs_dtype xt, 
     }
     return launch_status();
 }
+
+#include "norm_fp4_entry.cuh"

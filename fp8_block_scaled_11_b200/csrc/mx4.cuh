@@ -1,0 +1,80 @@
+// mx4.cuh -- microscaled 4-bit values: E2M1 codes in groups of 32 along K, each
+// group with one power-of-two scale held as a biased exponent (UE8M0).
+//
+// The scale rule: r = the smallest power of two with max|v| <= 6 r over the
+// group (max|v| taken as at least 1e-12), so that no value saturates; the code
+// is v / r rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (ties to the
+// even code), its highest bit the sign.  v / r is exact in fp32 (r is a power of
+// two), so the code has a single rounding.
+//
+// Packed matrix (rows x K): row-major, two codes to a byte, the even column in
+// the low half.  Scale tiles: one 512-byte tile per 128 rows x 4 groups (128
+// columns), tiles of a row block one after another along K; inside a tile the
+// byte of row r, group g is at (r % 32) * 16 + (r / 32 % 4) * 4 + g % 4, which
+// is the order in which the tensor cores' scale-factor copy reads it: a product
+// moves whole tiles and rearranges nothing.
+#pragma once
+
+#include <cstdint>
+#include "ptx.cuh"
+
+namespace fp8bs {
+
+constexpr uint32_t kSfTileBytes = 512;
+
+// The scale's byte for a group's largest magnitude (finite, >= 0).
+// max|v| = 1.m * 2^e fits 6 r = 1.5 * 2^2 * r: r = 2^(e - 2), or twice that
+// where 1.m > 1.5.  The floor of 1e-12 keeps the byte at 85 or more; the
+// largest finite fp32 gives 253.
+__device__ __forceinline__ uint32_t mx4_scale_byte(float amax)
+{
+    const uint32_t b = __float_as_uint(fmaxf(amax, 1e-12f));
+    return (b >> 23) - 2u + ((b & 0x7FFFFFu) > 0x400000u ? 1u : 0u);
+}
+
+// 1 / r of a scale byte in [1, 253].
+__device__ __forceinline__ float mx4_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// r of any scale byte: 2^(byte - 127) (byte 0 is subnormal in fp32), 255 is NaN.
+__device__ __forceinline__ float mx4_scale_value(uint32_t byte)
+{
+    return __uint_as_float(byte == 255u ? 0x7FFFFFFFu : byte == 0u ? 0x400000u : byte << 23);
+}
+
+// Eight values times s -> eight codes, value 0 in the lowest four bits.
+__device__ __forceinline__ uint32_t mx4_pack8(const float (&f)[8], float s)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(f[0] * s), "f"(f[1] * s), "f"(f[2] * s), "f"(f[3] * s), "f"(f[4] * s), "f"(f[5] * s), "f"(f[6] * s),
+          "f"(f[7] * s));
+    return r;
+}
+
+// Eight codes -> eight values times r (exact: a code's value has two bits).
+__device__ __forceinline__ void mx4_unpack8(uint32_t w, float r, float (&f)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t c = (w >> (4 * i)) & 15u;
+        // E2M1 -> fp32: exponent bias 1 -> 127; codes 0 and 1 (0 and 0.5) are the subnormals
+        const uint32_t m = c & 7u;
+        const float mag = m < 2u ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
+        f[i] = __uint_as_float(__float_as_uint(mag * r) | (c >> 3) << 31);
+    }
+}
+
+// Byte offset of the four scale bytes (one 128-column chunk) of row r, chunk kc,
+// in a matrix with `kcs` chunks per row.
+__device__ __forceinline__ int64_t sf_word_offset(int64_t r, int64_t kc, int64_t kcs)
+{
+    return ((r >> 7) * kcs + kc) * (int64_t)kSfTileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+}
+
+}  // namespace fp8bs

@@ -1,0 +1,372 @@
+// norm_fp4_entry.cuh -- C entry points of the RMS norm (norm_kernels.cuh), of the
+// microscaled 4-bit quantisation (fp4_quant_kernels.cuh) and of the 4-bit product
+// (gemm_fp4_kernel.cuh): argument validation and launches.  Part of fp8bs_lib.cu's
+// translation unit, whose helpers it uses.
+
+namespace {
+
+inline int64_t round32(int64_t v) { return (v + 31) / 32 * 32; }
+
+// ---------------------------------------------------------------- RMS norm
+// The arguments both forward entry points share.
+fp8bs_status check_norm(const NormParams& p, fp8bs_dtype xt, fp8bs_dtype wt)
+{
+    if (!valid_dtype(xt) || !valid_dtype(wt)) return FP8BS_ERR_UNSUPPORTED;
+    if (p.x == nullptr || p.w == nullptr || p.q == nullptr || p.scale == nullptr || p.rows < 1 || p.cols < 1)
+        return FP8BS_ERR_INVALID_ARG;
+    if (p.rows > INT32_MAX || p.cols > INT32_MAX) return FP8BS_ERR_INVALID_ARG;
+    if (!(p.eps >= 0.f)) return FP8BS_ERR_INVALID_ARG;
+    // the sum and h come together: without a residual h is x
+    if ((p.res == nullptr) != (p.h == nullptr)) return FP8BS_ERR_INVALID_ARG;
+    if (p.ldx < p.cols || (p.res != nullptr && (p.ldr < p.cols || p.ldh < p.cols)) ||
+        (p.y != nullptr && p.ldy < p.cols))
+        return FP8BS_ERR_INVALID_ARG;
+    const int64_t e = (int64_t)dtype_size(xt);
+    if (!aligned16(p.x) || !aligned16(p.res) || !aligned16(p.h) || !aligned16(p.w) || !aligned16(p.y) ||
+        !aligned16(p.q) || !aligned16(p.scale) || (reinterpret_cast<uintptr_t>(p.rstd) & 3))
+        return FP8BS_ERR_ALIGNMENT;
+    if ((p.ldx * e) % 16 || p.ldq % 16) return FP8BS_ERR_ALIGNMENT;
+    if (p.res != nullptr && ((p.ldr * e) % 16 || (p.ldh * e) % 16)) return FP8BS_ERR_ALIGNMENT;
+    if (p.y != nullptr && (p.ldy * e) % 16) return FP8BS_ERR_ALIGNMENT;
+    return FP8BS_OK;
+}
+
+template <typename T, int BITS>
+fp8bs_status launch_norm(DeviceInfo* d, const NormParams& p, cudaStream_t stream)
+{
+    const int64_t eights = cdiv(p.cols, 8);
+    // eights per thread: one where few rows leave the GPU idle otherwise (a row's
+    // latency is what counts), four where many rows keep it busy
+    const int vpt = p.rows <= 2 * d->num_sms && eights <= 1024 ? 1 : eights <= 4 * 512 ? 4 : 0;
+    if (vpt == 0) {
+        rmsnorm_quant_wide_kernel<T, BITS><<<(unsigned)p.rows, 512, 0, stream>>>(p);
+        return launch_status();
+    }
+    const int64_t tx = round32(cdiv(eights, vpt));
+    const int64_t ty = std::max<int64_t>(1, std::min<int64_t>(256 / tx, p.rows));
+    const dim3 block((unsigned)tx, (unsigned)ty);
+    const unsigned grid = (unsigned)cdiv(p.rows, ty);
+    if (vpt == 1) rmsnorm_quant_kernel<T, BITS, 1><<<grid, block, 0, stream>>>(p);
+    else rmsnorm_quant_kernel<T, BITS, 4><<<grid, block, 0, stream>>>(p);
+    return launch_status();
+}
+
+// The backward's launch: threads per row, rows per CTA, CTAs, and the bytes of
+// its workspace.  Rows of up to 8192 columns are read once (kBackVpt eights a
+// thread); wider ones take two launches.
+constexpr int kBackVpt = 2;
+constexpr int64_t kBackParts = 1024;            // rows of partial sums at most
+
+struct BackPlan {
+    bool wide;
+    int64_t tx, ty, grid, parts;
+    size_t dot_off, bytes;
+};
+
+BackPlan plan_back(int64_t rows, int64_t cols, int num_sms)
+{
+    BackPlan b;
+    const int64_t eights = cdiv(cols, 8);
+    b.wide = eights > kBackVpt * 512;
+    if (b.wide) {
+        b.tx = 256;
+        b.ty = 1;
+        b.grid = std::max<int64_t>(1, std::min<int64_t>(rows, 8 * num_sms / cdiv(cols, 2048)));
+        b.parts = b.grid;
+    } else {
+        b.tx = round32(cdiv(eights, kBackVpt));
+        b.ty = std::max<int64_t>(1, std::min<int64_t>(256 / b.tx, rows));
+        const int64_t per_sm = std::max<int64_t>(1, 1024 / (b.tx * b.ty));
+        b.grid = std::min<int64_t>({cdiv(rows, b.ty), per_sm * num_sms, kBackParts / b.ty});
+        b.parts = b.grid * b.ty;
+    }
+    b.dot_off = (size_t)(b.parts * cols) * sizeof(float);
+    b.bytes = b.dot_off + (b.wide ? (size_t)((rows + 3) / 4 * 4) * sizeof(float) : 0);
+    return b;
+}
+
+template <typename T>
+fp8bs_status launch_norm_back(const BackPlan& b, const NormBackParams& p, float* dweight, cudaStream_t stream)
+{
+    if (b.wide) {
+        rmsnorm_back_dot_kernel<T><<<(unsigned)p.rows, 512, 0, stream>>>(p);
+        const dim3 grid((unsigned)cdiv(p.cols, 2048), (unsigned)b.grid);
+        rmsnorm_back_wide_kernel<T><<<grid, 256, 0, stream>>>(p);
+    } else {
+        rmsnorm_back_kernel<T, kBackVpt><<<(unsigned)b.grid, dim3((unsigned)b.tx, (unsigned)b.ty), 0, stream>>>(p);
+    }
+    rmsnorm_dw_kernel<<<(unsigned)cdiv(p.cols, 32), 256, 0, stream>>>(p.part, (int)b.parts, p.cols, dweight);
+    return launch_status();
+}
+
+// ---------------------------------------------------------------- 4-bit product
+struct Fp4Plan {
+    int bn;
+    int tiles_m, tiles_n, splits;
+    int64_t ldw;
+    size_t ws_bytes;
+};
+
+Fp4Plan plan_fp4(int64_t M, int64_t N, int64_t K, int num_sms)
+{
+    Fp4Plan s;
+    s.tiles_n = (int)cdiv(N, kF4Rows);
+    // the narrowest tile that holds every token; 256 columns once they fill the GPU
+    s.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 || s.tiles_n * cdiv(M, 256) < num_sms ? 128 : 256;
+    s.tiles_m = (int)cdiv(M, s.bn);
+    const int64_t tiles = (int64_t)s.tiles_m * s.tiles_n;
+    const int64_t steps = cdiv(K, kF4StepK);
+    int splits = 1;
+    if (tiles * 2 <= num_sms) {
+        // fill the SMs, with at least four steps (16 KB of weights each) per split
+        splits = (int)std::min<int64_t>(num_sms / tiles, std::max<int64_t>(1, steps / 4));
+        splits = std::max(1, std::min(splits, 64));
+    }
+    s.splits = splits;
+    s.ldw = (N + 3) & ~int64_t(3);
+    s.ws_bytes = splits > 1 ? (size_t)splits * (size_t)M * (size_t)s.ldw * sizeof(float) : 0;
+    return s;
+}
+
+template <int BN>
+fp8bs_status launch_fp4(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap& tT, const Fp4Params& p,
+                        cudaStream_t stream)
+{
+    auto k = gemm_fp4_kernel<BN>;
+    constexpr int slot = BN == 16 ? 0 : BN == 32 ? 1 : BN == 64 ? 2 : BN == 128 ? 3 : 4;
+    if (!d->fp4_attr_set[slot].load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        if (!d->fp4_attr_set[slot].load(std::memory_order_relaxed)) {
+            if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Fp4Cfg<BN>::alloc) !=
+                cudaSuccess)
+                return FP8BS_ERR_CUDA;
+            d->fp4_attr_set[slot].store(true, std::memory_order_release);
+        }
+    }
+    const int grid = (int)std::min<int64_t>(p.num_units, d->num_sms);
+    k<<<grid, Fp4Cfg<BN>::threads, Fp4Cfg<BN>::alloc, stream>>>(tW, tT, p);
+    return launch_status();
+}
+
+// The split-K reduction, as a programmatic dependent of the product.
+fp8bs_status launch_reduce(DeviceInfo* d, const float* ws, int splits, int64_t M, int64_t N, int64_t ldw, void* D,
+                           int64_t ldd, int out_f32, int vec_out, cudaStream_t stream)
+{
+    const int64_t chunks = M * ((N + 3) / 4);
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(chunks, kReduceThreads), (int64_t)d->num_sms * 16));
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(kReduceThreads, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, splitk_reduce_kernel, ws, splits, M, N, ldw, D, ldd, out_f32, vec_out) != cudaSuccess)
+        return FP8BS_ERR_CUDA;
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8bs_status fp8_rmsnorm_quant_1x128(const void* x, int64_t ldx, const void* residual, int64_t ld_res, fp8bs_dtype xt,
+                                     int64_t rows, int64_t cols, const void* weight, fp8bs_dtype wt, float eps,
+                                     void* h, int64_t ldh, float* rstd, void* y, int64_t ldy, uint8_t* q, int64_t ldq,
+                                     float* scale_inv, int64_t ld_scale, fp8bs_scale_rule rule, cudaStream_t stream)
+{
+    if (rule != FP8BS_SCALE_RULE_FP32 && rule != FP8BS_SCALE_RULE_POW2) return FP8BS_ERR_UNSUPPORTED;
+    const NormParams p = {x, residual, weight, h, rstd, y, q, scale_inv, rows, cols, ldx, ld_res, ldh, ldy, ldq,
+                          ld_scale, eps, wt == FP8BS_F32, rule == FP8BS_SCALE_RULE_POW2};
+    fp8bs_status st = check_norm(p, xt, wt);
+    if (st != FP8BS_OK) return st;
+    if (ldq < cols || ld_scale < rows) return FP8BS_ERR_INVALID_ARG;
+    if (cols % 16 || ld_scale % 4) return FP8BS_ERR_ALIGNMENT;
+    DeviceInfo* d = nullptr;
+    if ((st = get_device(&d)) != FP8BS_OK) return st;
+    return xt == FP8BS_BF16 ? launch_norm<__nv_bfloat16, 8>(d, p, stream) : launch_norm<float, 8>(d, p, stream);
+}
+
+fp8bs_status fp4_rmsnorm_quant_1x32(const void* x, int64_t ldx, const void* residual, int64_t ld_res, fp8bs_dtype xt,
+                                    int64_t rows, int64_t cols, const void* weight, fp8bs_dtype wt, float eps,
+                                    void* h, int64_t ldh, float* rstd, void* y, int64_t ldy, uint8_t* q, int64_t ldq,
+                                    uint8_t* scale_tiles, cudaStream_t stream)
+{
+    const NormParams p = {x, residual, weight, h, rstd, y, q, scale_tiles, rows, cols, ldx, ld_res, ldh, ldy, ldq,
+                          cdiv(cols, 128), eps, wt == FP8BS_F32, 0};
+    fp8bs_status st = check_norm(p, xt, wt);
+    if (st != FP8BS_OK) return st;
+    if (cols % 32) return FP8BS_ERR_ALIGNMENT;
+    if (ldq < cols / 2) return FP8BS_ERR_INVALID_ARG;
+    DeviceInfo* d = nullptr;
+    if ((st = get_device(&d)) != FP8BS_OK) return st;
+    return xt == FP8BS_BF16 ? launch_norm<__nv_bfloat16, 4>(d, p, stream) : launch_norm<float, 4>(d, p, stream);
+}
+
+size_t fp8bs_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols)
+{
+    if (rows < 1 || cols < 1) return 0;
+    return plan_back(rows, cols, num_sms_current()).bytes;
+}
+
+fp8bs_status fp8bs_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* dh,
+                                    int64_t lddh, fp8bs_dtype xt, int64_t rows, int64_t cols, const void* weight,
+                                    fp8bs_dtype wt, const float* rstd, void* dx, int64_t lddx, float* dweight,
+                                    void* workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    if (!valid_dtype(xt) || !valid_dtype(wt)) return FP8BS_ERR_UNSUPPORTED;
+    if (dy == nullptr || h == nullptr || weight == nullptr || rstd == nullptr || dx == nullptr || dweight == nullptr ||
+        rows < 1 || cols < 1 || rows > INT32_MAX || cols > INT32_MAX)
+        return FP8BS_ERR_INVALID_ARG;
+    if (lddy < cols || ldh < cols || lddx < cols || (dh != nullptr && lddh < cols)) return FP8BS_ERR_INVALID_ARG;
+    const int64_t e = (int64_t)dtype_size(xt);
+    if (!aligned16(dy) || !aligned16(h) || !aligned16(dh) || !aligned16(weight) || !aligned16(dx) ||
+        (reinterpret_cast<uintptr_t>(rstd) & 3) || (reinterpret_cast<uintptr_t>(dweight) & 3))
+        return FP8BS_ERR_ALIGNMENT;
+    if ((lddy * e) % 16 || (ldh * e) % 16 || (lddx * e) % 16 || (dh != nullptr && (lddh * e) % 16) || cols % 16)
+        return FP8BS_ERR_ALIGNMENT;
+    DeviceInfo* d = nullptr;
+    fp8bs_status st = get_device(&d);
+    if (st != FP8BS_OK) return st;
+    const BackPlan b = plan_back(rows, cols, d->num_sms);
+    if (workspace == nullptr || workspace_bytes < b.bytes) return FP8BS_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return FP8BS_ERR_ALIGNMENT;
+    const NormBackParams p = {dy, h, dh, weight, rstd, dx, static_cast<float*>(workspace),
+                              reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + b.dot_off), rows, cols, lddy,
+                              ldh, lddh, lddx, wt == FP8BS_F32};
+    return xt == FP8BS_BF16 ? launch_norm_back<__nv_bfloat16>(b, p, dweight, stream)
+                            : launch_norm_back<float>(b, p, dweight, stream);
+}
+
+size_t fp4_scale_tiles_size(int64_t rows, int64_t cols)
+{
+    if (rows < 1 || cols < 1) return 0;
+    return (size_t)cdiv(rows, 128) * (size_t)cdiv(cols, 128) * kSfTileBytes;
+}
+
+fp8bs_status fp4_quant_1x32(const void* x, fp8bs_dtype xt, int64_t rows, int64_t cols, int64_t ldx, uint8_t* q,
+                            int64_t ldq, uint8_t* scale_tiles, int transpose_out, cudaStream_t stream)
+{
+    if (!valid_dtype(xt)) return FP8BS_ERR_UNSUPPORTED;
+    if (x == nullptr || q == nullptr || scale_tiles == nullptr || rows < 1 || cols < 1 || rows > INT32_MAX ||
+        cols > INT32_MAX || (transpose_out != 0 && transpose_out != 1) || ldx < cols)
+        return FP8BS_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(scale_tiles) || (ldx * (int64_t)dtype_size(xt)) % 16 || ldq % 16)
+        return FP8BS_ERR_ALIGNMENT;
+    if (transpose_out ? (rows % 32 || cols % 16) : cols % 32) return FP8BS_ERR_ALIGNMENT;
+    if (ldq < (transpose_out ? rows : cols) / 2) return FP8BS_ERR_INVALID_ARG;
+    DeviceInfo* d = nullptr;
+    fp8bs_status st = get_device(&d);
+    if (st != FP8BS_OK) return st;
+    const int64_t rb = cdiv(rows, 128), cb = cdiv(cols, 128);
+    if (rb * cb > INT32_MAX) return FP8BS_ERR_INVALID_ARG;
+    const unsigned grid = (unsigned)(rb * cb);
+    if (!transpose_out) {
+        if (xt == FP8BS_BF16)
+            fp4_quant_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(x), rows, cols, ldx, q,
+                                                            ldq, scale_tiles, cb);
+        else
+            fp4_quant_rows_kernel<<<grid, 256, 0, stream>>>(static_cast<const float*>(x), rows, cols, ldx, q, ldq,
+                                                            scale_tiles, cb);
+    } else {
+        if (xt == FP8BS_BF16)
+            fp4_quant_cols_kernel<<<grid, 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(x), rows, cols, ldx, q,
+                                                            ldq, scale_tiles, rb, cb);
+        else
+            fp4_quant_cols_kernel<<<grid, 256, 0, stream>>>(static_cast<const float*>(x), rows, cols, ldx, q, ldq,
+                                                            scale_tiles, rb, cb);
+    }
+    return launch_status();
+}
+
+fp8bs_status fp4_dequant_1x32(const uint8_t* q, int64_t ldq, const uint8_t* scale_tiles, int64_t rows, int64_t cols,
+                              void* out, fp8bs_dtype ot, int64_t ldo, cudaStream_t stream)
+{
+    if (!valid_dtype(ot)) return FP8BS_ERR_UNSUPPORTED;
+    if (q == nullptr || scale_tiles == nullptr || out == nullptr || rows < 1 || cols < 1 || rows > INT32_MAX ||
+        cols > INT32_MAX || ldq < cols / 2 || ldo < cols)
+        return FP8BS_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(scale_tiles) || !aligned16(out) || ldq % 16 ||
+        (ldo * (int64_t)dtype_size(ot)) % 16 || cols % 32)
+        return FP8BS_ERR_ALIGNMENT;
+    DeviceInfo* d = nullptr;
+    fp8bs_status st = get_device(&d);
+    if (st != FP8BS_OK) return st;
+    const int64_t total = rows * (cols / 8);
+    const unsigned grid = (unsigned)std::min<int64_t>(cdiv(total, 256), (int64_t)d->num_sms * 64);
+    if (ot == FP8BS_BF16)
+        fp4_dequant_kernel<<<grid, 256, 0, stream>>>(q, ldq, scale_tiles, rows, cols, cdiv(cols, 128),
+                                                     static_cast<__nv_bfloat16*>(out), ldo);
+    else
+        fp4_dequant_kernel<<<grid, 256, 0, stream>>>(q, ldq, scale_tiles, rows, cols, cdiv(cols, 128),
+                                                     static_cast<float*>(out), ldo);
+    return launch_status();
+}
+
+size_t fp4_scaled_gemm_workspace_size(int64_t M, int64_t N, int64_t K)
+{
+    if (M < 1 || N < 1 || K < 1) return 0;
+    return plan_fp4(M, N, K, num_sms_current()).ws_bytes;
+}
+
+fp8bs_status fp4_scaled_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda, const uint8_t* Bt,
+                             int64_t ldb, const uint8_t* scale_a, const uint8_t* scale_b, void* D, int64_t ldd,
+                             fp8bs_dtype out_dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    if (!valid_dtype(out_dtype)) return FP8BS_ERR_UNSUPPORTED;
+    if (A == nullptr || Bt == nullptr || scale_a == nullptr || scale_b == nullptr || D == nullptr || M < 1 || N < 1 ||
+        K < 32 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX)
+        return FP8BS_ERR_INVALID_ARG;
+    if (lda < K / 2 || ldb < K / 2 || ldd < N) return FP8BS_ERR_INVALID_ARG;
+    if (K % 32 || lda % 16 || ldb % 16 || !aligned16(A) || !aligned16(Bt) || !aligned16(scale_a) ||
+        !aligned16(scale_b) || reinterpret_cast<uintptr_t>(D) % dtype_size(out_dtype))
+        return FP8BS_ERR_ALIGNMENT;
+    DeviceInfo* d = nullptr;
+    fp8bs_status st = get_device(&d);
+    if (st != FP8BS_OK) return st;
+    Fp4Plan plan = plan_fp4(M, N, K, d->num_sms);
+    if (plan.splits > 1) {
+        if (workspace == nullptr && workspace_bytes == 0) plan.splits = 1;      // split-K disabled by the caller
+        else if (workspace == nullptr || workspace_bytes < plan.ws_bytes) return FP8BS_ERR_WORKSPACE;
+        else if (!aligned16(workspace)) return FP8BS_ERR_ALIGNMENT;
+    }
+    CUtensorMap tW, tT;
+    if ((st = make_map(&tW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Bt, K / 2, N, ldb, 128, kF4Rows,
+                       CU_TENSOR_MAP_SWIZZLE_128B)) != FP8BS_OK)
+        return st;
+    if ((st = make_map(&tT, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A, K / 2, M, lda, 128, (uint32_t)plan.bn,
+                       CU_TENSOR_MAP_SWIZZLE_128B)) != FP8BS_OK)
+        return st;
+    Fp4Params p;
+    p.M = (int32_t)M;
+    p.N = (int32_t)N;
+    p.K = (int32_t)K;
+    p.steps = (int32_t)cdiv(K, kF4StepK);
+    p.kcs = (int32_t)cdiv(K, 128);
+    p.tiles_m = plan.tiles_m;
+    p.tiles_n = plan.tiles_n;
+    p.splits = plan.splits;
+    p.num_units = (int64_t)plan.tiles_m * plan.tiles_n * plan.splits;
+    p.sfa = scale_a;
+    p.sfb = scale_b;
+    p.D = D;
+    p.ldd = ldd;
+    p.out_f32 = out_dtype == FP8BS_F32;
+    p.ws = static_cast<float*>(workspace);
+    p.ldw = plan.ldw;
+    p.err = d->err_ptr;
+    switch (plan.bn) {
+    case 16: st = launch_fp4<16>(d, tW, tT, p, stream); break;
+    case 32: st = launch_fp4<32>(d, tW, tT, p, stream); break;
+    case 64: st = launch_fp4<64>(d, tW, tT, p, stream); break;
+    case 128: st = launch_fp4<128>(d, tW, tT, p, stream); break;
+    default: st = launch_fp4<256>(d, tW, tT, p, stream); break;
+    }
+    if (st != FP8BS_OK || plan.splits == 1) return st;
+    const int vec_out = aligned16(D) && (ldd * (int64_t)dtype_size(out_dtype)) % 16 == 0;
+    return launch_reduce(d, p.ws, plan.splits, M, N, plan.ldw, D, ldd, p.out_f32, vec_out, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,54 @@
+// ptx_fp4.cuh -- inline-PTX wrappers of the 4-bit block-scaled MMA (sm_100a) and
+// of the untiled bulk copy that brings its scale tiles.  Single instructions, as
+// in ptx.cuh.
+#pragma once
+
+#include <cstdint>
+#include "ptx.cuh"
+#include "ptx_bs.cuh"
+
+namespace fp8bs {
+
+// kind::mxf4.block_scale, scale_vec::2X: E2M1 x E2M1 -> F32, K = 64 per
+// instruction, one UE8M0 factor per 32 K.  Instruction descriptor: bits [4,6)
+// the B scale-factor id, [7,10) the A format (E2M1 = 1), [10,12) the B format,
+// 15 / 16 A / B major (K = 0), [17,23) N >> 3, bit 23 the scale type (1 =
+// UE8M0), [27,29) M >> 7, [29,31) the A scale-factor id, bit 31 the K size (0 =
+// 64).  The id (0 or 2) names the first of the two bytes of each 32-bit TMEM
+// scale-factor word that this MMA uses.
+__host__ __device__ constexpr uint32_t idesc_e2m1_bs(uint32_t M, uint32_t N, uint32_t sf_id)
+{
+    return (sf_id << 4)
+         | (1u << 7) | (1u << 10)
+         | (0u << 15) | (0u << 16)
+         | ((N >> 3) << 17)
+         | (1u << 23)
+         | ((M >> 7) << 27)
+         | (sf_id << 29);
+}
+
+// D[tmem] (+)= (A[smem] . B[smem]^T), each product of 32 K scaled by its rows'
+// factors at sfa / sfb in TMEM (the byte id also in bits [30,32) of these
+// addresses).
+__device__ __forceinline__ void umma_f4_bs(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t sfa, uint32_t sfb, uint32_t accum)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accum), "r"(sfa), "r"(sfb)
+        : "memory");
+}
+
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned,
+// counted on mbarrier `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+}  // namespace fp8bs

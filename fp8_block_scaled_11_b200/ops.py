@@ -74,6 +74,19 @@ def lib():
                                               i64, i32, p]
         L.fp8_scaled_gemm_quant.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i64, i32, i32, p, i64,
                                             p, i64, p, i64, p]
+        f32 = ctypes.c_float
+        norm = [p, i64, p, i64, i32, i64, i64, p, i32, f32, p, i64, p, p, i64, p, i64, p]
+        L.fp8_rmsnorm_quant_1x128.argtypes = norm + [i64, i32, p]
+        L.fp4_rmsnorm_quant_1x32.argtypes = norm + [p]
+        L.fp8bs_rmsnorm_backward_workspace_size.argtypes = [i64, i64]
+        L.fp8bs_rmsnorm_backward.argtypes = [p, i64, p, i64, p, i64, i32, i64, i64, p, i32, p, p, i64, p, p, sz, p]
+        L.fp4_scale_tiles_size.argtypes = [i64, i64]
+        L.fp4_quant_1x32.argtypes = [p, i32, i64, i64, i64, p, i64, p, i32, p]
+        L.fp4_dequant_1x32.argtypes = [p, i64, p, i64, i64, p, i32, i64, p]
+        L.fp4_scaled_gemm_workspace_size.argtypes = [i64, i64, i64]
+        L.fp4_scaled_gemm.argtypes = [i64, i64, i64, p, i64, p, i64, p, p, p, i64, i32, p, sz, p]
+        for fn in ("fp8bs_rmsnorm_backward_workspace_size", "fp4_scale_tiles_size", "fp4_scaled_gemm_workspace_size"):
+            getattr(L, fn).restype = sz
         L.fp8bs_status_string.argtypes = [i32]
         L.fp8bs_status_string.restype = ctypes.c_char_p
         L.fp8bs_check_device_error.argtypes = [p]
@@ -81,7 +94,9 @@ def lib():
         for fn in ("fp8_quant_1x128", "fp8_quant_1x128_dual", "fp8_quant_128x128", "fp8_quant_1x128_ex",
                    "fp8_quant_1x128_dual_ex", "fp8_quant_128x128_ex", "fp8_quant_tensor",
                    "fp8_quant_rowwise", "fp8_scaled_gemm", "fp8_scaled_gemm_ex", "fp8_scaled_gemm_quant", "fp8_scaled_gemm_grouped",
-                   "fp8bs_check_device_error", "fp8_quant_tensor_noalloc"):
+                   "fp8bs_check_device_error", "fp8_quant_tensor_noalloc", "fp8_rmsnorm_quant_1x128",
+                   "fp4_rmsnorm_quant_1x32", "fp8bs_rmsnorm_backward", "fp4_quant_1x32", "fp4_dequant_1x32",
+                   "fp4_scaled_gemm"):
             getattr(L, fn).restype = i32
         _lib = L
     return _lib
@@ -383,6 +398,197 @@ def fp8_scaled_gemm_quant(A: torch.Tensor, Bt: torch.Tensor, scale_a: torch.Tens
                                        q_out.data_ptr(), q_out.stride(0), scale_out.data_ptr(),
                                        _grid_ld(scale_out, M), _stream(A)))
     return out, q_out, scale_out
+
+
+# ---------------------------------------------------------------------------- microscaled 4 bits
+def fp4_scale_tiles(rows: int, cols: int, device) -> torch.Tensor:
+    """Allocate the scale tiles of a rows x cols matrix of 4-bit codes: a uint8
+    tensor (ceil(rows/128), ceil(cols/128), 32, 4, 4) whose element [i//128,
+    g//4, i%32, i//32%4, g%4] is the scale byte of row i, group g (32 columns)."""
+    return torch.empty(((rows + 127) // 128, (cols + 127) // 128, 32, 4, 4), dtype=torch.uint8, device=device)
+
+
+def _codes(q: torch.Tensor, what: str):
+    """rows, codes per row and the leading dimension (bytes) of packed codes."""
+    if q.dtype != torch.uint8:
+        raise TypeError(f"{what}: packed 4-bit codes are uint8")
+    return q.shape[0], 2 * q.shape[1], _ld(q)
+
+
+def _tiles(s: torch.Tensor, rows: int, cols: int, device, what: str) -> int:
+    if (s.dtype != torch.uint8 or s.device != device or not s.is_contiguous()
+            or s.numel() != (rows + 127) // 128 * ((cols + 127) // 128) * 512):
+        raise ValueError(f"{what}: expected the fp4_scale_tiles of a {rows} x {cols} matrix on {device}")
+    return s.data_ptr()
+
+
+def _on(t: torch.Tensor, device, what: str, shape=None, dtype=None) -> int:
+    """t's address, after its device, shape and dtype are checked."""
+    if t.device != device or (shape is not None and tuple(t.shape) != shape) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what}: expected {shape or 'a tensor'} {dtype or ''} on {device}, got {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def fp4_quant_1x32(x: torch.Tensor, transpose_out: bool = False, q: Optional[torch.Tensor] = None,
+                   scale: Optional[torch.Tensor] = None):
+    """Microscaled 4-bit quantization: returns (q uint8 rows x cols/2, scale
+    tiles).  transpose_out=False: groups of 32 along the columns of x (cols %
+    32 == 0).  transpose_out=True: groups along its rows (rows % 32 == 0); q is
+    cols x rows/2.  Preallocated outputs may be passed as q / scale."""
+    rows, cols = x.shape
+    xt = _dtype_code(x)
+    R, C = (cols, rows) if transpose_out else (rows, cols)
+    if q is None:
+        # rows of bytes start 16-byte aligned
+        q = torch.empty((R, _round_up(C // 2, 16)), dtype=torch.uint8, device=x.device)[:, :C // 2]
+    if scale is None:
+        scale = fp4_scale_tiles(R, C, x.device)
+    _check("fp4_quant_1x32", lib().fp4_quant_1x32(x.data_ptr(), xt, rows, cols, _ld(x),
+                                                  _on(q, x.device, "q", (R, C // 2), torch.uint8), _ld(q),
+                                                  _tiles(scale, R, C, x.device, "scale"), int(transpose_out),
+                                                  _stream(x)))
+    return q, scale
+
+
+def fp4_dequant_1x32(q: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values of packed 4-bit codes and their scale tiles."""
+    rows, cols, ldq = _codes(q, "q")
+    if out is None:
+        out = torch.empty((rows, cols), dtype=out_dtype, device=q.device)
+    _check("fp4_dequant_1x32", lib().fp4_dequant_1x32(q.data_ptr(), ldq, _tiles(scale, rows, cols, q.device, "scale"),
+                                                      rows, cols, _on(out, q.device, "out", (rows, cols)),
+                                                      _dtype_code(out), _ld(out), _stream(q)))
+    return out
+
+
+def fp4_scaled_gemm_workspace(M: int, N: int, K: int, device) -> Optional[torch.Tensor]:
+    """Allocate the split-K workspace of a product of these sizes (None where it needs none)."""
+    n = int(lib().fp4_scaled_gemm_workspace_size(M, N, K))
+    return torch.empty((n,), dtype=torch.uint8, device=device) if n else None
+
+
+def fp4_scaled_gemm(A: torch.Tensor, Bt: torch.Tensor, scale_a: torch.Tensor, scale_b: torch.Tensor,
+                    out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, split_k: bool = True) -> torch.Tensor:
+    """D = A . Bt^T of two microscaled 4-bit matrices: A M x K/2 and Bt N x K/2
+    uint8 (two codes a byte) with their scale tiles, as fp4_quant_1x32 returns
+    them.  D: M x N, bf16 or fp32."""
+    M, K, lda = _codes(A, "A")
+    N, K2, ldb = _codes(Bt, "Bt")
+    if K2 != K:
+        raise ValueError("A and Bt must share K")
+    dev = A.device
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    if split_k and workspace is None:
+        workspace = fp4_scaled_gemm_workspace(M, N, K, dev)
+    wp, wn = ((_on(workspace, dev, "workspace"), workspace.numel() * workspace.element_size())
+              if split_k and workspace is not None else (0, 0))
+    _check("fp4_scaled_gemm", lib().fp4_scaled_gemm(M, N, K, A.data_ptr(), lda, _on(Bt, dev, "Bt"), ldb,
+                                                    _tiles(scale_a, M, K, dev, "scale_a"),
+                                                    _tiles(scale_b, N, K, dev, "scale_b"),
+                                                    _on(out, dev, "out", (M, N)), _ld(out), _dtype_code(out), wp, wn,
+                                                    _stream(A)))
+    return out
+
+
+# ---------------------------------------------------------------------------- RMS norm
+def rmsnorm_quant_buffers(x: torch.Tensor, residual: bool = False, want_y: bool = False, bits: int = 8):
+    """Allocate the outputs of fp8_rmsnorm_quant_1x128 (bits = 8) or
+    fp4_rmsnorm_quant_1x32 (bits = 4) for inputs like x: (q, scale, h, rstd, y),
+    h and y None where they are not asked for."""
+    rows, cols = x.shape
+    dev = x.device
+    if bits == 8:
+        q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+        s = colmajor_grid(rows, (cols + 127) // 128, dev)
+    else:
+        q = torch.empty((rows, _round_up(cols // 2, 16)), dtype=torch.uint8, device=dev)[:, :cols // 2]
+        s = fp4_scale_tiles(rows, cols, dev)
+    new = lambda: torch.empty((rows, cols), dtype=x.dtype, device=dev)  # noqa: E731
+    return (q, s, new() if residual else None, torch.empty((rows,), dtype=torch.float32, device=dev),
+            new() if want_y else None)
+
+
+def _rmsnorm_quant(fn, bits, x, weight, residual, eps, want_y, out, tail):
+    rows, cols = x.shape
+    xt, dev = _dtype_code(x), x.device
+    if out is None:
+        out = rmsnorm_quant_buffers(x, residual is not None, want_y, bits)
+    q, s, h, rstd, y = out
+    if (h is None) != (residual is None):
+        raise ValueError(f"{fn}: out has h exactly where there is a residual")
+    shape, dt = (rows, cols), x.dtype
+    rp = lr = hp = lh = yp = ly = 0
+    if residual is not None:
+        rp, lr = _on(residual, dev, "residual", shape, dt), _ld(residual)
+        hp, lh = _on(h, dev, "h", shape, dt), _ld(h)
+    if y is not None:
+        yp, ly = _on(y, dev, "y", shape, dt), _ld(y)
+    if not weight.is_contiguous() or not rstd.is_contiguous():
+        raise ValueError(f"{fn}: weight and rstd must be contiguous")
+    _check(fn, getattr(lib(), fn)(x.data_ptr(), _ld(x), rp, lr, xt, rows, cols, _on(weight, dev, "weight", (cols,)),
+                                  _dtype_code(weight), eps, hp, lh, _on(rstd, dev, "rstd", (rows,), torch.float32), yp,
+                                  ly, _on(q, dev, "q", (rows, cols * bits // 8), torch.uint8), _ld(q), *tail(s)))
+    return q, s, x if residual is None else h, rstd, y
+
+
+def fp8_rmsnorm_quant_1x128(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                            eps: float = 1e-6, want_y: bool = False, out=None, rule: int = SCALE_RULE_FP32):
+    """RMS norm of h = x + residual with its result quantized 1x128 in e4m3:
+    returns (q, scale_inv grid, h, rstd, y); h is x without a residual, y (the
+    norm's value in x's dtype) None unless want_y.  Preallocated outputs may be
+    passed as out (rmsnorm_quant_buffers); h may be x or residual itself."""
+    dev = x.device
+
+    def tail(s):
+        return (_on(s, dev, "scale_inv", (x.shape[0], (x.shape[1] + 127) // 128), torch.float32),
+                _grid_ld(s, x.shape[0]), int(rule), _stream(x))
+    return _rmsnorm_quant("fp8_rmsnorm_quant_1x128", 8, x, weight, residual, eps, want_y, out, tail)
+
+
+def fp4_rmsnorm_quant_1x32(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                           eps: float = 1e-6, want_y: bool = False, out=None):
+    """fp8_rmsnorm_quant_1x128 with its result in microscaled 4 bits: q is rows x
+    cols/2 packed codes, the scales are scale tiles (bits=4 buffers)."""
+    def tail(s):
+        return _tiles(s, x.shape[0], x.shape[1], x.device, "scale"), _stream(x)
+    return _rmsnorm_quant("fp4_rmsnorm_quant_1x32", 4, x, weight, residual, eps, want_y, out, tail)
+
+
+def rmsnorm_backward_workspace(h: torch.Tensor) -> torch.Tensor:
+    """Allocate the workspace of fp8bs_rmsnorm_backward for inputs like h."""
+    n = int(lib().fp8bs_rmsnorm_backward_workspace_size(h.shape[0], h.shape[1]))
+    return torch.empty((n,), dtype=torch.uint8, device=h.device)
+
+
+def fp8bs_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                           dh: Optional[torch.Tensor] = None, out=None, workspace: Optional[torch.Tensor] = None):
+    """Gradients of the norm: returns (dx, dweight fp32) from dy (the gradient of
+    y), the forward pass's h and rstd, and dh (the gradient that reaches h past
+    the norm; added to dx).  Preallocated outputs may be passed as out=(dx,
+    dweight); dx may be dy, dh or h itself."""
+    rows, cols = h.shape
+    xt, dev = _dtype_code(h), h.device
+    shape, dt = (rows, cols), h.dtype
+    dx, dw = out if out is not None else (torch.empty(shape, dtype=dt, device=dev),
+                                          torch.empty((cols,), dtype=torch.float32, device=dev))
+    if workspace is None:
+        workspace = rmsnorm_backward_workspace(h)
+    gp, lg = (_on(dh, dev, "dh", shape, dt), _ld(dh)) if dh is not None else (0, 0)
+    if not (weight.is_contiguous() and rstd.is_contiguous() and dw.is_contiguous()):
+        raise ValueError("fp8bs_rmsnorm_backward: weight, rstd and dweight must be contiguous")
+    _check("fp8bs_rmsnorm_backward",
+           lib().fp8bs_rmsnorm_backward(_on(dy, dev, "dy", shape, dt), _ld(dy), h.data_ptr(), _ld(h), gp, lg, xt, rows,
+                                        cols, _on(weight, dev, "weight", (cols,)), _dtype_code(weight),
+                                        _on(rstd, dev, "rstd", (rows,), torch.float32),
+                                        _on(dx, dev, "dx", shape, dt), _ld(dx),
+                                        _on(dw, dev, "dweight", (cols,), torch.float32),
+                                        _on(workspace, dev, "workspace"),
+                                        workspace.numel() * workspace.element_size(), _stream(h)))
+    return dx, dw
 
 
 def fp8bs_status_string(status: int) -> str:

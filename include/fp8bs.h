@@ -411,6 +411,136 @@ fp8bs_status fp8_scaled_gemm_grouped(int64_t groups, const int64_t* group_rows, 
                                      int64_t sb_group_stride, fp8bs_scale_mode mode, fp8bs_scale_layout layout,
                                      void* D, int64_t ldd, fp8bs_dtype out_dtype, cudaStream_t stream);
 
+/*
+ * fp8_rmsnorm_quant_1x128, fp4_rmsnorm_quant_1x32 -- the root-mean-square norm
+ * in front of a linear layer, with the residual's addition before it and its
+ * result quantized for the layer's GEMM, in one pass over memory.
+ *
+ *   h    = x + residual, rounded to x's type (without a residual h is x);
+ *   rstd = 1 / sqrt(mean_j h[j]^2 + eps), per row, from the rounded h;
+ *   y    = h * rstd * weight, in fp32;
+ *   q    = y quantized from fp32 (not from a rounded y): 1x128 groups along the
+ *          row by the rule of fp8_quant_1x128 (`rule` as fp8_quant_1x128_ex),
+ *          the A operand of fp8_scaled_gemm; or groups of 32 in microscaled 4
+ *          bits by the rule of fp4_quant_1x32, the A operand of fp4_scaled_gemm.
+ *
+ * x            rows x cols, dtype xt (bf16 or fp32), leading dim ldx.
+ * residual     nullable; rows x cols, dtype xt, leading dim ld_res.
+ * weight       cols elements of dtype wt (bf16 or fp32).
+ * h            rows x cols, dtype xt, leading dim ldh: the new residual stream,
+ *              required with a residual, NULL without one.  h may be x or
+ *              residual (same pointer and leading dim).
+ * rstd         nullable; rows floats (what the backward pass takes).
+ * y            nullable; rows x cols, dtype xt: y rounded to xt, leading dim ldy.
+ * q            8 bits: rows x cols e4m3 bytes, leading dim ldq >= cols, with
+ *              scale_inv[r + g*ld_scale] as fp8_quant_1x128.
+ *              4 bits: rows x cols/2 bytes, leading dim ldq >= cols/2, with
+ *              scale tiles as fp4_quant_1x32.
+ * Any number of rows >= 1; cols % 16 == 0 (8 bits) or cols % 32 == 0 (4 bits).
+ * x, residual, weight, h, y, q and the scales 16-byte aligned, rstd 4-byte;
+ * leading dims in bytes multiples of 16; ld_scale % 4 == 0.  eps >= 0; eps = 0
+ * with an all-zero row divides by zero.  Inputs must be finite, and a row's sum
+ * of squares must fit fp32.  Errors as the quantizations.
+ */
+fp8bs_status fp8_rmsnorm_quant_1x128(const void* x, int64_t ldx, const void* residual, int64_t ld_res, fp8bs_dtype xt,
+                                     int64_t rows, int64_t cols, const void* weight, fp8bs_dtype wt, float eps,
+                                     void* h, int64_t ldh, float* rstd, void* y, int64_t ldy, uint8_t* q, int64_t ldq,
+                                     float* scale_inv, int64_t ld_scale, fp8bs_scale_rule rule, cudaStream_t stream);
+fp8bs_status fp4_rmsnorm_quant_1x32(const void* x, int64_t ldx, const void* residual, int64_t ld_res, fp8bs_dtype xt,
+                                    int64_t rows, int64_t cols, const void* weight, fp8bs_dtype wt, float eps,
+                                    void* h, int64_t ldh, float* rstd, void* y, int64_t ldy, uint8_t* q, int64_t ldq,
+                                    uint8_t* scale_tiles, cudaStream_t stream);
+
+/*
+ * fp8bs_rmsnorm_backward -- the gradients of the norm above (the quantization
+ * counts as the identity: dy is the gradient of y, as the linear layer's dgrad
+ * GEMM writes it).  With n = h * rstd and g = dy * weight:
+ *
+ *   dx      = rstd * (g - n * mean_j(g[j] n[j])) + dh     (fp32, rounded once)
+ *   dweight = sum over the rows of dy * n                 (fp32)
+ *
+ * dx is the gradient of h, hence of x and of the residual alike.
+ *
+ * dy, h        rows x cols, dtype xt, leading dims lddy, ldh; h and rstd as the
+ *              forward pass left them.
+ * dh           nullable; rows x cols, dtype xt, leading dim lddh: the gradient
+ *              that reaches h past the norm, through the residual stream.
+ * dx           rows x cols, dtype xt, leading dim lddx; may be dy, dh or h (same
+ *              pointer and leading dim).
+ * dweight      cols floats, overwritten.
+ * workspace    device scratch of at least
+ *              fp8bs_rmsnorm_backward_workspace_size(rows, cols) bytes, 16-byte
+ *              aligned; no initial contents needed.  Calls that may overlap on
+ *              the GPU need a workspace each.
+ * The rows' sums are added in an order that rows, cols and the device fix:
+ * results are deterministic.  cols % 16 == 0; alignment as the forward pass.
+ * FP8BS_ERR_WORKSPACE: no workspace, or too small a one.
+ */
+size_t fp8bs_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols);
+fp8bs_status fp8bs_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* dh,
+                                    int64_t lddh, fp8bs_dtype xt, int64_t rows, int64_t cols, const void* weight,
+                                    fp8bs_dtype wt, const float* rstd, void* dx, int64_t lddx, float* dweight,
+                                    void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fp4_quant_1x32 -- microscaled 4-bit quantization: E2M1 codes (0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 and their negatives) in groups of 32, each group with one
+ * power-of-two scale.
+ *
+ *   r = the smallest power of two with max(max|v|, 1e-12) <= 6 r over the group
+ *       (the largest power of two not above 6 / max|v|, inverted: the
+ *       power-of-two rule of the 8-bit formats with 6 for 448), so that no value
+ *       saturates;
+ *   code = v / r rounded to nearest, ties to the even code (sign in bit 3, -0 kept).
+ *
+ * transpose_out = 0: groups along the contiguous dim of x.  q: rows x cols/2
+ *            bytes, two codes each (the even column in the low four bits),
+ *            leading dim ldq >= cols/2.  cols % 32 == 0.
+ * transpose_out = 1: groups along the rows of x, the transpose is written.  q:
+ *            cols x rows/2 bytes, ldq >= rows/2.  rows % 32 == 0, cols % 16 == 0.
+ * scale_tiles  fp4_scale_tiles_size(R, C) bytes for the R x C matrix of codes
+ *            (R = rows, C = cols, or the reverse when transposed): one byte per
+ *            group, the biased exponent e of r = 2^(e - 127), in 512-byte tiles
+ *            of 128 rows x 4 groups; the byte of row i, group g is at
+ *              ((i/128) * ceil(C/128) + g/4) * 512 + (i%32)*16 + (i/32%4)*4 + g%4.
+ *            Groups past C in a row's last four get e = 127; bytes of rows past R
+ *            are left as they were, and nothing reads them.
+ * x, q, scale_tiles 16-byte aligned; ldx in bytes and ldq multiples of 16.
+ *
+ * fp4_dequant_1x32 -- the values of such a matrix (rows x cols codes), exact in
+ * bf16 or fp32 (dtype ot) wherever they are in the type's range.  cols % 32 == 0;
+ * out 16-byte aligned, ldo in bytes a multiple of 16.
+ */
+size_t fp4_scale_tiles_size(int64_t rows, int64_t cols);
+fp8bs_status fp4_quant_1x32(const void* x, fp8bs_dtype xt, int64_t rows, int64_t cols, int64_t ldx, uint8_t* q,
+                            int64_t ldq, uint8_t* scale_tiles, int transpose_out, cudaStream_t stream);
+fp8bs_status fp4_dequant_1x32(const uint8_t* q, int64_t ldq, const uint8_t* scale_tiles, int64_t rows, int64_t cols,
+                              void* out, fp8bs_dtype ot, int64_t ldo, cudaStream_t stream);
+
+/*
+ * fp4_scaled_gemm -- D = A . Bt^T of two microscaled 4-bit matrices (the "TN"
+ * layout of F.linear), accumulated in fp32 on the tensor cores' block-scaled MMA.
+ *
+ * A, scale_a   M x K codes, leading dim lda bytes, and their scale tiles
+ *              (fp4_quant_1x32, fp4_rmsnorm_quant_1x32).
+ * Bt, scale_b  N x K codes, leading dim ldb bytes, and their scale tiles.
+ *              A scale byte of 255 is NaN, as in the format.
+ * D            M x N, dtype out_dtype (bf16 rounded to nearest even, or fp32),
+ *              leading dim ldd elements; any ldd >= N.
+ * workspace    optional fp32 scratch for split-K (used when the output has few
+ *              tiles): NULL/0 to disable split-K, or at least
+ *              fp4_scaled_gemm_workspace_size(M, N, K) bytes, 16-byte aligned.
+ *              Partial sums are added in a fixed order: results are
+ *              deterministic.  Calls that may overlap on the GPU need a
+ *              workspace each.
+ * Any M, N >= 1; K >= 32, K % 32 == 0.  A, Bt, scale_a, scale_b 16-byte aligned;
+ * lda, ldb multiples of 16; D aligned to its element size.
+ */
+size_t fp4_scaled_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
+fp8bs_status fp4_scaled_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda, const uint8_t* Bt,
+                             int64_t ldb, const uint8_t* scale_a, const uint8_t* scale_b, void* D, int64_t ldd,
+                             fp8bs_dtype out_dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* fp8bs_status_string(fp8bs_status s);
 
