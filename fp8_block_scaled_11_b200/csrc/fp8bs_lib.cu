@@ -25,6 +25,7 @@
 #include "norm_kernels.cuh"
 #include "fp4_quant_kernels.cuh"
 #include "gemm_fp4_kernel.cuh"
+#include "gemm_fp4_pair_kernel.cuh"
 
 using namespace fp8bs;
 
@@ -48,7 +49,8 @@ struct DeviceInfo {
     std::atomic<bool> tile_attr_set[16]{};   // per tile kernel kind (+8: power-of-two scale rule)
     std::atomic<int> tile_blocks[16]{};
     std::atomic<int> pair_clusters[8]{};     // co-resident CTA pairs, per pair-kernel instantiation
-    std::atomic<bool> fp4_attr_set[5]{};     // 4-bit product, per tile width
+    std::atomic<bool> fp4_attr_set[4]{};     // 4-bit product on single CTAs, per tile width
+    std::atomic<int> fp4_pair_clusters{};    // 4-bit product on CTA pairs: co-resident pairs
 };
 
 DeviceInfo g_dev[kMaxDevices];

@@ -51,6 +51,7 @@ struct Fp4Params {
     int32_t kcs;                // scale tiles per 128 rows: ceil(K / 128)
     int32_t tiles_m, tiles_n;
     int32_t splits;
+    int32_t band;               // weight tiles per band of the tile order
     int64_t num_units;          // tiles_m * tiles_n * splits
     const uint8_t* sfa;         // scale tiles of A (tokens) and of B^T
     const uint8_t* sfb;
@@ -89,16 +90,17 @@ struct Fp4Cfg {
     static_assert(t_off % 1024 == 0 && t_bytes % 1024 == 0, "swizzled tiles 1024-byte aligned");
 };
 
-// Unit u: bands of 16 weight tiles, all token tiles of a band before the next
+// Unit u: bands of p.band weight tiles, all token tiles of a band before the next
 // band, so that concurrent CTAs share both operands in L2.
 __device__ __forceinline__ void fp4_unit(const Fp4Params& p, int64_t u, int& tm, int& tn, int& s0, int& s1, int& split)
 {
     const int64_t tile = u / p.splits;
     split = (int)(u - tile * p.splits);
-    const int64_t band = tile / (16 * (int64_t)p.tiles_m);
-    const int64_t in = tile - band * 16 * p.tiles_m;
-    const int n0 = (int)band * 16;
-    const int width = min(16, p.tiles_n - n0);
+    const int64_t per_band = (int64_t)p.band * p.tiles_m;
+    const int64_t band = tile / per_band;
+    const int64_t in = tile - band * per_band;
+    const int n0 = (int)band * p.band;
+    const int width = min(p.band, p.tiles_n - n0);
     tn = n0 + (int)(in % width);
     tm = (int)(in / width);
     s0 = (int)(((int64_t)p.steps * split) / p.splits);

@@ -101,6 +101,7 @@ fp8bs_status launch_norm_back(const BackPlan& b, const NormBackParams& p, float*
 
 // ---------------------------------------------------------------- 4-bit product
 struct Fp4Plan {
+    bool pair;                  // 256 x 256 tiles on CTA pairs; else 128 x bn tiles on single CTAs
     int bn;
     int tiles_m, tiles_n, splits;
     int64_t ldw;
@@ -110,14 +111,15 @@ struct Fp4Plan {
 Fp4Plan plan_fp4(int64_t M, int64_t N, int64_t K, int num_sms)
 {
     Fp4Plan s;
-    s.tiles_n = (int)cdiv(N, kF4Rows);
-    // the narrowest tile that holds every token; 256 columns once they fill the GPU
-    s.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 || s.tiles_n * cdiv(M, 256) < num_sms ? 128 : 256;
+    s.pair = M > 128 && cdiv(N, kF4Pair) * cdiv(M, kF4Pair) >= num_sms / 2;
+    s.tiles_n = (int)cdiv(N, s.pair ? kF4Pair : kF4Rows);
+    // single CTAs: the narrowest tile that holds every token
+    s.bn = s.pair ? kF4Pair : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     s.tiles_m = (int)cdiv(M, s.bn);
     const int64_t tiles = (int64_t)s.tiles_m * s.tiles_n;
     const int64_t steps = cdiv(K, kF4StepK);
     int splits = 1;
-    if (tiles * 2 <= num_sms) {
+    if (!s.pair && tiles * 2 <= num_sms) {
         // fill the SMs, with at least four steps (16 KB of weights each) per split
         splits = (int)std::min<int64_t>(num_sms / tiles, std::max<int64_t>(1, steps / 4));
         splits = std::max(1, std::min(splits, 64));
@@ -133,7 +135,7 @@ fp8bs_status launch_fp4(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap&
                         cudaStream_t stream)
 {
     auto k = gemm_fp4_kernel<BN>;
-    constexpr int slot = BN == 16 ? 0 : BN == 32 ? 1 : BN == 64 ? 2 : BN == 128 ? 3 : 4;
+    constexpr int slot = BN == 16 ? 0 : BN == 32 ? 1 : BN == 64 ? 2 : 3;
     if (!d->fp4_attr_set[slot].load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> lock(g_mutex);
         if (!d->fp4_attr_set[slot].load(std::memory_order_relaxed)) {
@@ -145,6 +147,49 @@ fp8bs_status launch_fp4(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap&
     }
     const int grid = (int)std::min<int64_t>(p.num_units, d->num_sms);
     k<<<grid, Fp4Cfg<BN>::threads, Fp4Cfg<BN>::alloc, stream>>>(tW, tT, p);
+    return launch_status();
+}
+
+fp8bs_status launch_fp4_pair(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap& tT, const Fp4Params& p,
+                             cudaStream_t stream)
+{
+    // scale tiles as rows of 128-row blocks of 32-bit words: two tiles (1024
+    // bytes, the chunks of a step) of one block of B^T, of two blocks of A
+    CUtensorMap tSW, tST;
+    fp8bs_status st = make_map(&tSW, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, p.sfb, (uint64_t)p.kcs * 128, cdiv(p.N, 128),
+                               (uint64_t)p.kcs * kSfTileBytes, 256, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (st == FP8BS_OK)
+        st = make_map(&tST, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, p.sfa, (uint64_t)p.kcs * 128, cdiv(p.M, 128),
+                      (uint64_t)p.kcs * kSfTileBytes, 256, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (st != FP8BS_OK) return st;
+    auto k = gemm_fp4_pair_kernel;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kF4PairThreads, 1, 1);
+    cfg.dynamicSmemBytes = Fp4PairSmem::alloc;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int nc = d->fp4_pair_clusters.load(std::memory_order_acquire);
+    if (nc == 0) {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        nc = d->fp4_pair_clusters.load(std::memory_order_relaxed);
+        if (nc == 0) {
+            if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Fp4PairSmem::alloc) !=
+                cudaSuccess)
+                return FP8BS_ERR_CUDA;
+            cfg.gridDim = dim3(2 * std::max(1, d->num_sms / 2), 1, 1);
+            if (cudaOccupancyMaxActiveClusters(&nc, k, &cfg) != cudaSuccess) return FP8BS_ERR_CUDA;
+            if (nc < 1) return FP8BS_ERR_UNSUPPORTED;
+            d->fp4_pair_clusters.store(nc, std::memory_order_release);
+        }
+    }
+    cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(p.num_units, nc)), 1, 1);
+    if (cudaLaunchKernelEx(&cfg, k, tW, tT, tSW, tST, p) != cudaSuccess) return FP8BS_ERR_CUDA;
     return launch_status();
 }
 
@@ -336,7 +381,8 @@ fp8bs_status fp4_scaled_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* A, 
     if ((st = make_map(&tW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Bt, K / 2, N, ldb, 128, kF4Rows,
                        CU_TENSOR_MAP_SWIZZLE_128B)) != FP8BS_OK)
         return st;
-    if ((st = make_map(&tT, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A, K / 2, M, lda, 128, (uint32_t)plan.bn,
+    if ((st = make_map(&tT, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A, K / 2, M, lda, 128,
+                       (uint32_t)(plan.pair ? kF4Rows : plan.bn),
                        CU_TENSOR_MAP_SWIZZLE_128B)) != FP8BS_OK)
         return st;
     Fp4Params p;
@@ -348,6 +394,7 @@ fp8bs_status fp4_scaled_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* A, 
     p.tiles_m = plan.tiles_m;
     p.tiles_n = plan.tiles_n;
     p.splits = plan.splits;
+    p.band = plan.pair ? 8 : 16;
     p.num_units = (int64_t)plan.tiles_m * plan.tiles_n * plan.splits;
     p.sfa = scale_a;
     p.sfb = scale_b;
@@ -357,12 +404,12 @@ fp8bs_status fp4_scaled_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* A, 
     p.ws = static_cast<float*>(workspace);
     p.ldw = plan.ldw;
     p.err = d->err_ptr;
+    if (plan.pair) return launch_fp4_pair(d, tW, tT, p, stream);
     switch (plan.bn) {
     case 16: st = launch_fp4<16>(d, tW, tT, p, stream); break;
     case 32: st = launch_fp4<32>(d, tW, tT, p, stream); break;
     case 64: st = launch_fp4<64>(d, tW, tT, p, stream); break;
-    case 128: st = launch_fp4<128>(d, tW, tT, p, stream); break;
-    default: st = launch_fp4<256>(d, tW, tT, p, stream); break;
+    default: st = launch_fp4<128>(d, tW, tT, p, stream); break;
     }
     if (st != FP8BS_OK || plan.splits == 1) return st;
     const int vec_out = aligned16(D) && (ldd * (int64_t)dtype_size(out_dtype)) % 16 == 0;

@@ -136,7 +136,8 @@ def check(got, a, b, out_dtype, k, splits=64):
 
 SHAPES = [(1, 1, 32), (1, 5120, 8192), (7, 130, 96), (16, 128, 256), (17, 1000, 288), (33, 257, 4128), (64, 512, 512),
           (65, 300, 160), (128, 128, 2048), (129, 384, 1056), (200, 640, 224), (256, 4096, 1024), (300, 1000, 2080),
-          (777, 1000, 2080), (1024, 19000, 64)]
+          (777, 1000, 2080), (1024, 19000, 64), (129, 19000, 96), (2300, 2304, 288),
+          (5000, 1100, 544), (2305, 2050, 4128), (70, 19000, 160)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
