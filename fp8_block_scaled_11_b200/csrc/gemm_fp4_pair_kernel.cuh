@@ -13,19 +13,19 @@
 // 325 with none).
 //
 // Roles, per CTA of the cluster of two (rank 0 = leader), 16 warps:
-//   warps 0, 3   TMA producers of the even / odd steps (256 K each): this CTA's
-//                128 rows of B^T and of A (128-byte swizzle), completing on the
-//                leader's stage barrier, and the scale tiles of its B^T rows and of
-//                all 256 rows of A, completing on its own.
+//   warps 0, 3   TMA producers of B^T / of A, per step (512 K): this CTA's 128 rows
+//                of the operand (128-byte swizzle, two 128-byte halves), completing
+//                on the leader's stage barrier, and the scale tiles of its rows of
+//                B^T / of all 256 rows of A, completing on its own.
 //   warp 1       TMEM allocation (both CTAs); in the leader, lane 0 issues the
-//                pair MMAs, four 256x256x64 per step.
+//                pair MMAs, eight 256x256x64 per step.
 //   warps 4-11   epilogue: warp w reads lanes 32 (w % 4) .. +31 and 128 of the
 //                256 columns, rounds to bf16 in registers, releases the
 //                accumulator and stores.
 //   warps 12-15  scale-factor writers.
 // A stage's TMEM scale columns are written again only after the MMAs that read
 // them have completed: the writers follow a refill, which follows the commit.
-// TMEM: the 256-column accumulator, then kF4PairStages x 24 scale columns.
+// TMEM: the 256-column accumulator, then kF4PairStages x 48 scale columns.
 //
 // Every wait is bounded as in gemm_pair_kernel.cuh; a wait that runs out stops
 // both CTAs' roles.
@@ -44,10 +44,12 @@
 namespace fp8bs {
 
 constexpr int kF4Pair = 256;                    // rows of B^T and of A per tile
-constexpr int kF4PairStages = 6;
-constexpr uint32_t kF4PairTile = 128 * 128;     // one operand's 128 rows x 128 bytes
-constexpr uint32_t kF4PairSf = 3 * 2 * kSfTileBytes;   // B^T's block, A's two blocks, two tiles (chunks) each
-constexpr uint32_t kF4PairSfCols = 24;
+constexpr int kF4PairStepK = 512;               // K per step
+constexpr int kF4PairStages = 3;
+constexpr uint32_t kF4PairHalf = 128 * 128;     // one operand's 128 rows x 128 bytes (256 K)
+constexpr uint32_t kF4PairTile = 2 * kF4PairHalf;
+constexpr uint32_t kF4PairSf = 3 * 4 * kSfTileBytes;   // B^T's block, A's two blocks, four tiles (128 K each) each
+constexpr uint32_t kF4PairSfCols = 48;
 constexpr int kF4PairEpiWarps = 8;
 constexpr int kF4PairThreads = 32 * (4 + kF4PairEpiWarps + 4);
 static_assert(kF4Pair + kF4PairStages * kF4PairSfCols <= kTmemCols, "scale factors exceed TMEM");
@@ -57,8 +59,8 @@ struct Fp4PairSmem {
     static constexpr uint32_t t_off = w_off + kF4PairStages * kF4PairTile;
     static constexpr uint32_t sf_off = t_off + kF4PairStages * kF4PairTile;
     static constexpr uint32_t bar_off = sf_off + kF4PairStages * kF4PairSf;
-    // ab_full[S], ab_empty[S], sl_full[S] (scale tiles landed), sf_full[S] (scale columns written), tm_full, tm_empty, drain
-    static constexpr uint32_t n_bars = 4 * kF4PairStages + 3;
+    // ab_full[S] (operands landed, scale columns written), ab_empty[S], sl_full[S] (scale tiles landed), tm_full, tm_empty, drain
+    static constexpr uint32_t n_bars = 3 * kF4PairStages + 3;
     static constexpr uint32_t misc_off = bar_off + n_bars * 8;
     static constexpr uint32_t alloc = misc_off + 16 + 1024;
 };
@@ -78,8 +80,7 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
     auto ab_full = [&](int s) { return bars + 8u * s; };
     auto ab_empty = [&](int s) { return bars + 8u * (kStages + s); };
     auto sl_full = [&](int s) { return bars + 8u * (2 * kStages + s); };
-    auto sf_full = [&](int s) { return bars + 8u * (3 * kStages + s); };
-    const uint32_t tm_full = bars + 8u * (4 * kStages);
+    const uint32_t tm_full = bars + 8u * (3 * kStages);
     const uint32_t tm_empty = tm_full + 8u;
     const uint32_t drain_bar = tm_full + 16u;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + S::misc_off);
@@ -94,10 +95,9 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(ab_full(s), 1);
+            mbar_init(ab_full(s), 2 + 2 * 4);          // the leader's producers and both CTAs' writer warps
             mbar_init(ab_empty(s), 1);
-            mbar_init(sl_full(s), 1);
-            mbar_init(sf_full(s), 2 * 4);              // both CTAs' writer warps
+            mbar_init(sl_full(s), 2);
         }
         mbar_init(tm_full, 1);
         mbar_init(tm_empty, 2 * kF4PairEpiWarps);      // both CTAs' epilogue warps
@@ -129,32 +129,37 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
     };
 
     if (warp == 0 || warp == 3) {
-        // ---------------------------------------------------------------- producers (even / odd steps)
+        // ---------------------------------------------------------------- producers (B^T, A)
         if (lane == 0) {
-            const int t = warp == 0 ? 0 : 1;
+            const bool wside = warp == 0;
+            const CUtensorMap* map = wside ? &tmW : &tmT;
+            const CUtensorMap* smap = wside ? &tmSW : &tmST;
+            const uint32_t dst0 = sbase + (wside ? S::w_off : S::t_off);
+            const uint32_t sf0 = sbase + S::sf_off + (wside ? 0u : 4 * kSfTileBytes);
+            const uint32_t sf_bytes = (wside ? 4u : 8u) * kSfTileBytes;
             bool ok = true;
-            uint32_t filled = 0, fill_par = 0;     // per stage: ever filled by this thread, parity of its latest fill
-            int64_t seq = 0;                       // steps of this cluster so far
+            uint32_t filled = 0, fill_par = 0;     // per stage: ever filled, parity of its latest fill
+            int stage = 0;
+            uint32_t phase = 0;
             for (int64_t u = cluster_id; u < p.num_units && ok; u += num_clusters) {
                 int tm, tn, s0, s1, split;
                 fp4_unit(p, u, tm, tn, s0, s1, split);
-                const int n0 = tn * kF4Pair + (int)rank * 128;        // this CTA's rows of B^T
-                const int m0 = tm * kF4Pair + (int)rank * 128;        // and of A
-                for (int st = s0; st < s1; ++st, ++seq) {
-                    if ((int)(seq & 1) != t) continue;
-                    const int stage = (int)(seq % kStages);
-                    const uint32_t phase = (uint32_t)((seq / kStages) & 1);
-                    if (!mbar_wait_bounded(ab_empty(stage), phase ^ 1u, abort_flag, kWaitLimitNs)) { ok = false; break; }
-                    if (leader) mbar_arrive_expect_tx(ab_full(stage), 4 * kF4PairTile);
-                    mbar_arrive_expect_tx(sl_full(stage), kF4PairSf);
-                    const uint32_t sf = sbase + S::sf_off + stage * kF4PairSf;
-                    tma_load_2d(sf, &tmSW, sl_full(stage), st * 256, n0 >> 7);
-                    tma_load_2d(sf + 2 * kSfTileBytes, &tmST, sl_full(stage), st * 256, tm * 2);
+                const int tile = wside ? tn : tm;
+                const int row0 = tile * kF4Pair + (int)rank * 128;     // this CTA's rows of the operand
+                // scale tiles: of this CTA's rows of B^T, of all the tile's rows of A
+                const int block = wside ? row0 >> 7 : tile * 2;
+                for (int st = s0; st < s1; ++st) {
+                    if (!mbar_wait_limit(ab_empty(stage), phase ^ 1u, abort_flag, kWaitLimitNs)) { ok = false; break; }
+                    if (leader) mbar_arrive_expect_tx(ab_full(stage), 2 * kF4PairTile);
+                    mbar_arrive_expect_tx(sl_full(stage), sf_bytes);
+                    tma_load_2d(sf0 + stage * kF4PairSf, smap, sl_full(stage), st * 256, block);
                     const uint32_t full_leader = mapa_shared(ab_full(stage), 0);
-                    tma_load_2d_pair(sbase + S::w_off + stage * kF4PairTile, &tmW, full_leader, st * 128, n0);
-                    tma_load_2d_pair(sbase + S::t_off + stage * kF4PairTile, &tmT, full_leader, st * 128, m0);
+                    const uint32_t dst = dst0 + stage * kF4PairTile;
+                    tma_load_2d_pair(dst, map, full_leader, st * 256, row0);
+                    tma_load_2d_pair(dst + kF4PairHalf, map, full_leader, st * 256 + 128, row0);
                     filled |= 1u << stage;
                     fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
                 }
             }
             if (!ok) give_up();
@@ -181,24 +186,29 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
             for (int64_t u = cluster_id; u < p.num_units && ok; u += num_clusters) {
                 int tm, tn, s0, s1, split;
                 fp4_unit(p, u, tm, tn, s0, s1, split);
-                if (!mbar_wait_bounded(tm_empty, tphase ^ 1u, abort_flag, kWaitLimitNs)) { ok = false; break; }
+                if (!mbar_wait_limit(tm_empty, tphase ^ 1u, abort_flag, kWaitLimitNs)) { ok = false; break; }
                 for (int st = s0; st < s1; ++st) {
-                    if (!mbar_wait_bounded(sf_full(stage), phase, abort_flag, kWaitLimitNs) ||
-                        !mbar_wait_bounded(ab_full(stage), phase, abort_flag, kWaitLimitNs)) { ok = false; break; }
+                    if (!mbar_wait_limit(ab_full(stage), phase, abort_flag, kWaitLimitNs)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t sf = tmem_base + kF4Pair + (uint32_t)stage * kF4PairSfCols;
-                    const uint32_t w_addr = sbase + S::w_off + stage * kF4PairTile;
-                    const uint32_t t_addr = sbase + S::t_off + stage * kF4PairTile;
-                    const int mmas = min(4, (p.K - st * kF4StepK + kF4MmaK - 1) / kF4MmaK);
+                    const uint64_t wd = smem_desc_k_sw128(sbase + S::w_off + stage * kF4PairTile);
+                    const uint64_t td = smem_desc_k_sw128(sbase + S::t_off + stage * kF4PairTile);
+                    const int left = p.K - st * kF4PairStepK;
+                    // MMA k: 32 bytes further in the 128-byte rows, the second half after four; factor
+                    // bytes 0, 1 or 2, 3 of the words of chunk k / 2
+                    auto mma = [&](int k, uint32_t accum) {
+                        const uint64_t step = (uint64_t)((k & 3) * 2 + (k >> 2) * (int)(kF4PairHalf >> 4));
+                        const uint32_t id = (uint32_t)(k & 1) * 2u;
+                        const uint32_t col = (sf + (uint32_t)(k >> 1) * (kF4PairSfCols / 4)) | (id << 30);
+                        umma_f4_bs_pair(tmem_base, wd + step, td + step, idesc_e2m1_bs(kF4Pair, kF4Pair, id), col,
+                                        col + 4, accum);
+                    };
+                    if (left >= kF4PairStepK) {
+                        mma(0, st > s0 ? 1u : 0u);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k < mmas) {
-                            const uint32_t id = (uint32_t)(k & 1) * 2u;
-                            const uint32_t col = (sf + (uint32_t)(k >> 1) * (kF4PairSfCols / 2)) | (id << 30);
-                            umma_f4_bs_pair(tmem_base, smem_desc_k_sw128(w_addr + k * 32),
-                                            smem_desc_k_sw128(t_addr + k * 32), idesc_e2m1_bs(kF4Pair, kF4Pair, id), col,
-                                            col + 4, (st > s0 || k > 0) ? 1u : 0u);
-                        }
+                        for (int k = 1; k < 8; ++k) mma(k, 1u);
+                    } else {
+                        for (int k = 0; k * kF4MmaK < left; ++k) mma(k, (st > s0 || k > 0) ? 1u : 0u);
                     }
                     if (st + 1 == s1) umma_commit_pair_mc(tm_full, 0x3);
                     umma_commit_pair_mc(ab_empty(stage), 0x3);
@@ -221,7 +231,7 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
         for (int64_t u = cluster_id; u < p.num_units; u += num_clusters) {
             int tm, tn, s0, s1, split;
             fp4_unit(p, u, tm, tn, s0, s1, split);
-            if (!mbar_wait_bounded(tm_full, tphase, abort_flag, kWaitLimitNs)) ok = false;
+            if (!mbar_wait_limit(tm_full, tphase, abort_flag, kWaitLimitNs)) ok = false;
             tphase ^= 1u;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -284,32 +294,32 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
             int tm, tn, s0, s1, split;
             fp4_unit(p, u, tm, tn, s0, s1, split);
             for (int st = s0; st < s1; ++st) {
-                if (!mbar_wait_bounded(sl_full(stage), phase, abort_flag, kWaitLimitNs)) ok = false;
+                if (!mbar_wait_limit(sl_full(stage), phase, abort_flag, kWaitLimitNs)) ok = false;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 // lane l: row l of each tile (its four words are rows l, l + 32, ..); chunk c of the
                 // step: B^T's block, A's two blocks
                 const uint32_t src = sbase + S::sf_off + stage * kF4PairSf + (uint32_t)lane * 16u;
-                uint32_t r[24];
+                uint32_t r[48];
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int j = 0; j < 3; ++j) {
-                        const uint4 v = lds_u4(src + (2 * j + c) * kSfTileBytes);
+                        const uint4 v = lds_u4(src + (4 * j + c) * kSfTileBytes);
                         r[12 * c + 4 * j] = v.x;
                         r[12 * c + 4 * j + 1] = v.y;
                         r[12 * c + 4 * j + 2] = v.z;
                         r[12 * c + 4 * j + 3] = v.w;
                     }
                 const uint32_t dst = taddr + (uint32_t)stage * kF4PairSfCols;
-                tmem_st_32x32b_x16(dst, r);
-                tmem_st_32x32b_x8(dst + 16, r + 16);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) tmem_st_32x32b_x16(dst + 16 * i, r + 16 * i);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (leader) mbar_arrive(sf_full(stage));
-                    else mbar_arrive_remote(mapa_shared(sf_full(stage), 0));
+                    if (leader) mbar_arrive(ab_full(stage));
+                    else mbar_arrive_remote(mapa_shared(ab_full(stage), 0));
                 }
                 if (++stage == kStages) { stage = 0; phase ^= 1u; }
             }

@@ -153,13 +153,13 @@ fp8bs_status launch_fp4(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap&
 fp8bs_status launch_fp4_pair(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap& tT, const Fp4Params& p,
                              cudaStream_t stream)
 {
-    // scale tiles as rows of 128-row blocks of 32-bit words: two tiles (1024
+    // scale tiles as rows of 128-row blocks of 64-bit words: four tiles (2048
     // bytes, the chunks of a step) of one block of B^T, of two blocks of A
     CUtensorMap tSW, tST;
-    fp8bs_status st = make_map(&tSW, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, p.sfb, (uint64_t)p.kcs * 128, cdiv(p.N, 128),
+    fp8bs_status st = make_map(&tSW, CU_TENSOR_MAP_DATA_TYPE_INT64, 8, p.sfb, (uint64_t)p.kcs * 64, cdiv(p.N, 128),
                                (uint64_t)p.kcs * kSfTileBytes, 256, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (st == FP8BS_OK)
-        st = make_map(&tST, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, p.sfa, (uint64_t)p.kcs * 128, cdiv(p.M, 128),
+        st = make_map(&tST, CU_TENSOR_MAP_DATA_TYPE_INT64, 8, p.sfa, (uint64_t)p.kcs * 64, cdiv(p.M, 128),
                       (uint64_t)p.kcs * kSfTileBytes, 256, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (st != FP8BS_OK) return st;
     auto k = gemm_fp4_pair_kernel;
@@ -389,7 +389,7 @@ fp8bs_status fp4_scaled_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* A, 
     p.M = (int32_t)M;
     p.N = (int32_t)N;
     p.K = (int32_t)K;
-    p.steps = (int32_t)cdiv(K, kF4StepK);
+    p.steps = (int32_t)cdiv(K, plan.pair ? kF4PairStepK : kF4StepK);
     p.kcs = (int32_t)cdiv(K, 128);
     p.tiles_m = plan.tiles_m;
     p.tiles_n = plan.tiles_n;

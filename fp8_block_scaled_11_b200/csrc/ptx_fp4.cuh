@@ -55,7 +55,7 @@ __device__ __forceinline__ void umma_f4_bs_pair(uint32_t d_tmem, uint64_t adesc,
         : "memory");
 }
 
-// Thread i of the warp writes 16 (8) consecutive columns of TMEM lane
+// Thread i of the warp writes 16 consecutive columns of TMEM lane
 // lane_base + i; complete after tmem_st_wait.
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t* r)
 {
@@ -66,16 +66,27 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};"
-        ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_st_wait()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// mbar_wait_bounded that looks at the clock only every 64 tries (each try waits
+// inside the instruction for a while): the tries that find the phase complete,
+// nearly all of them, read no timer.
+__device__ __forceinline__ bool mbar_wait_limit(uint32_t bar, uint32_t parity, const volatile int* abort,
+                                                uint64_t limit_ns)
+{
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63u) == 0u) {
+            if (abort != nullptr && *abort) return false;
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > limit_ns) return false;
+        }
+    }
 }
 
 // `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned,

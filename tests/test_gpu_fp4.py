@@ -164,6 +164,17 @@ def test_product_exact(M, N, K):
     assert torch.equal(d, d2)
 
 
+@pytest.mark.parametrize("M,N,K", [(5000, 4200, 8192), (16640, 1300, 4128), (300, 40000, 1600)])
+def test_product_exact_large(M, N, K):
+    """Many tiles per CTA and many steps per tile, the reference in 64 bits on the GPU: exact as above."""
+    a, sa, av = operand(M, K, 51, spread=0)
+    b, sb, bv = operand(N, K, 52, spread=0)
+    want = (torch.from_numpy(av).cuda() @ torch.from_numpy(bv).cuda().t())
+    assert torch.equal(ops.fp4_scaled_gemm(a, b, sa, sb, out_dtype=torch.float32).double(), want)
+    assert torch.equal(ops.fp4_scaled_gemm(a, b, sa, sb), want.float().bfloat16())
+    no_device_error()
+
+
 @pytest.mark.parametrize("M,N,K,ldd", [(5, 70, 96, 75), (130, 257, 320, 301), (300, 130, 256, 131), (700, 515, 320, 517),
                                        (260, 20000, 96, 20004)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
