@@ -20,8 +20,8 @@
 //   warp 1       TMEM allocation (both CTAs); in the leader, lane 0 issues the
 //                pair MMAs, eight 256x256x64 per step.
 //   warps 4-11   epilogue: warp w reads lanes 32 (w % 4) .. +31 and 128 of the
-//                256 columns, rounds to bf16 in registers, releases the
-//                accumulator and stores.
+//                256 columns into registers, releases the accumulator,
+//                converts and stores.
 //   warps 12-15  scale-factor writers.
 // A stage's TMEM scale columns are written again only after the MMAs that read
 // them have completed: the writers follow a refill, which follows the commit.
@@ -52,6 +52,10 @@ constexpr uint32_t kF4PairSf = 3 * 4 * kSfTileBytes;   // B^T's block, A's two b
 constexpr uint32_t kF4PairSfCols = 48;
 constexpr int kF4PairEpiWarps = 8;
 constexpr int kF4PairThreads = 32 * (4 + kF4PairEpiWarps + 4);
+constexpr int kF4LaunchRegs = 128;              // registers per thread at launch (65536 / kF4PairThreads)
+constexpr int kF4CtrlRegs = 72;                 // after the hand-over: warps 0-3,
+constexpr int kF4WriterRegs = 88;               // scale-factor writers,
+constexpr int kF4EpiRegs = 176;                 // epilogue
 static_assert(kF4Pair + kF4PairStages * kF4PairSfCols <= kTmemCols, "scale factors exceed TMEM");
 
 struct Fp4PairSmem {
@@ -128,100 +132,107 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
         atomicOr(p.err, 1);
     };
 
-    if (warp == 0 || warp == 3) {
-        // ---------------------------------------------------------------- producers (B^T, A)
-        if (lane == 0) {
-            const bool wside = warp == 0;
-            const CUtensorMap* map = wside ? &tmW : &tmT;
-            const CUtensorMap* smap = wside ? &tmSW : &tmST;
-            const uint32_t dst0 = sbase + (wside ? S::w_off : S::t_off);
-            const uint32_t sf0 = sbase + S::sf_off + (wside ? 0u : 4 * kSfTileBytes);
-            const uint32_t sf_bytes = (wside ? 4u : 8u) * kSfTileBytes;
-            bool ok = true;
-            uint32_t filled = 0, fill_par = 0;     // per stage: ever filled, parity of its latest fill
-            int stage = 0;
-            uint32_t phase = 0;
-            for (int64_t u = cluster_id; u < p.num_units && ok; u += num_clusters) {
-                int tm, tn, s0, s1, split;
-                fp4_unit(p, u, tm, tn, s0, s1, split);
-                const int tile = wside ? tn : tm;
-                const int row0 = tile * kF4Pair + (int)rank * 128;     // this CTA's rows of the operand
-                // scale tiles: of this CTA's rows of B^T, of all the tile's rows of A
-                const int block = wside ? row0 >> 7 : tile * 2;
-                for (int st = s0; st < s1; ++st) {
-                    if (!mbar_wait_limit(ab_empty(stage), phase ^ 1u, abort_flag, kWaitLimitNs)) { ok = false; break; }
-                    if (leader) mbar_arrive_expect_tx(ab_full(stage), 2 * kF4PairTile);
-                    mbar_arrive_expect_tx(sl_full(stage), sf_bytes);
-                    tma_load_2d(sf0 + stage * kF4PairSf, smap, sl_full(stage), st * 256, block);
-                    const uint32_t full_leader = mapa_shared(ab_full(stage), 0);
-                    const uint32_t dst = dst0 + stage * kF4PairTile;
-                    tma_load_2d_pair(dst, map, full_leader, st * 256, row0);
-                    tma_load_2d_pair(dst + kF4PairHalf, map, full_leader, st * 256 + 128, row0);
-                    filled |= 1u << stage;
-                    fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
-                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
-                }
-            }
-            if (!ok) give_up();
-            // the loads this thread issued land before the CTA exits; after an
-            // abort a peer's load may target a phase the leader never armed, so
-            // stray loads also get a fixed time
-            for (int s = 0; s < kStages; ++s)
-                if (filled >> s & 1u) {
-                    mbar_wait_bounded(sl_full(s), fill_par >> s & 1u, nullptr, kDrainLimitNs);
-                    if (leader) mbar_wait_bounded(ab_full(s), fill_par >> s & 1u, nullptr, kDrainLimitNs);
-                }
-            if (*abort_flag) {
-                const uint64_t t0 = globaltimer_ns();
-                while (globaltimer_ns() - t0 < kPairAbortGraceNs) {
-                }
-            }
-        }
-    } else if (warp == 1) {
-        // ---------------------------------------------------------------- MMA issuer (leader)
-        if (leader && lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, tphase = 0;
-            bool ok = true;
-            for (int64_t u = cluster_id; u < p.num_units && ok; u += num_clusters) {
-                int tm, tn, s0, s1, split;
-                fp4_unit(p, u, tm, tn, s0, s1, split);
-                if (!mbar_wait_limit(tm_empty, tphase ^ 1u, abort_flag, kWaitLimitNs)) { ok = false; break; }
-                for (int st = s0; st < s1; ++st) {
-                    if (!mbar_wait_limit(ab_full(stage), phase, abort_flag, kWaitLimitNs)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t sf = tmem_base + kF4Pair + (uint32_t)stage * kF4PairSfCols;
-                    const uint64_t wd = smem_desc_k_sw128(sbase + S::w_off + stage * kF4PairTile);
-                    const uint64_t td = smem_desc_k_sw128(sbase + S::t_off + stage * kF4PairTile);
-                    const int left = p.K - st * kF4PairStepK;
-                    // MMA k: 32 bytes further in the 128-byte rows, the second half after four; factor
-                    // bytes 0, 1 or 2, 3 of the words of chunk k / 2
-                    auto mma = [&](int k, uint32_t accum) {
-                        const uint64_t step = (uint64_t)((k & 3) * 2 + (k >> 2) * (int)(kF4PairHalf >> 4));
-                        const uint32_t id = (uint32_t)(k & 1) * 2u;
-                        const uint32_t col = (sf + (uint32_t)(k >> 1) * (kF4PairSfCols / 4)) | (id << 30);
-                        umma_f4_bs_pair(tmem_base, wd + step, td + step, idesc_e2m1_bs(kF4Pair, kF4Pair, id), col,
-                                        col + 4, accum);
-                    };
-                    if (left >= kF4PairStepK) {
-                        mma(0, st > s0 ? 1u : 0u);
-#pragma unroll
-                        for (int k = 1; k < 8; ++k) mma(k, 1u);
-                    } else {
-                        for (int k = 0; k * kF4MmaK < left; ++k) mma(k, (st > s0 || k > 0) ? 1u : 0u);
+    // register hand-over: the launch's 128 a thread go to the epilogue's two
+    // warpgroups, whose 128 accumulator columns a thread stay in registers
+    static_assert(128 * (kF4CtrlRegs + kF4WriterRegs) + 256 * kF4EpiRegs <= kF4PairThreads * kF4LaunchRegs, "register hand-over");
+    if (warp < 4) {
+        setmaxnreg_dec<kF4CtrlRegs>();
+        if (warp == 0 || warp == 3) {
+            // ---------------------------------------------------------------- producers (B^T, A)
+            if (lane == 0) {
+                const bool wside = warp == 0;
+                const CUtensorMap* map = wside ? &tmW : &tmT;
+                const CUtensorMap* smap = wside ? &tmSW : &tmST;
+                const uint32_t dst0 = sbase + (wside ? S::w_off : S::t_off);
+                const uint32_t sf0 = sbase + S::sf_off + (wside ? 0u : 4 * kSfTileBytes);
+                const uint32_t sf_bytes = (wside ? 4u : 8u) * kSfTileBytes;
+                bool ok = true;
+                uint32_t filled = 0, fill_par = 0;     // per stage: ever filled, parity of its latest fill
+                int stage = 0;
+                uint32_t phase = 0;
+                for (int64_t u = cluster_id; u < p.num_units && ok; u += num_clusters) {
+                    int tm, tn, s0, s1, split;
+                    fp4_unit(p, u, tm, tn, s0, s1, split);
+                    const int tile = wside ? tn : tm;
+                    const int row0 = tile * kF4Pair + (int)rank * 128;     // this CTA's rows of the operand
+                    // scale tiles: of this CTA's rows of B^T, of all the tile's rows of A
+                    const int block = wside ? row0 >> 7 : tile * 2;
+                    for (int st = s0; st < s1; ++st) {
+                        if (!mbar_wait_limit(ab_empty(stage), phase ^ 1u, abort_flag, kWaitLimitNs)) { ok = false; break; }
+                        if (leader) mbar_arrive_expect_tx(ab_full(stage), 2 * kF4PairTile);
+                        mbar_arrive_expect_tx(sl_full(stage), sf_bytes);
+                        tma_load_2d(sf0 + stage * kF4PairSf, smap, sl_full(stage), st * 256, block);
+                        const uint32_t full_leader = mapa_shared(ab_full(stage), 0);
+                        const uint32_t dst = dst0 + stage * kF4PairTile;
+                        tma_load_2d_pair(dst, map, full_leader, st * 256, row0);
+                        tma_load_2d_pair(dst + kF4PairHalf, map, full_leader, st * 256 + 128, row0);
+                        filled |= 1u << stage;
+                        fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
+                        if (++stage == kStages) { stage = 0; phase ^= 1u; }
                     }
-                    if (st + 1 == s1) umma_commit_pair_mc(tm_full, 0x3);
-                    umma_commit_pair_mc(ab_empty(stage), 0x3);
-                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
                 }
-                tphase ^= 1u;
+                if (!ok) give_up();
+                // the loads this thread issued land before the CTA exits; after an
+                // abort a peer's load may target a phase the leader never armed, so
+                // stray loads also get a fixed time
+                for (int s = 0; s < kStages; ++s)
+                    if (filled >> s & 1u) {
+                        mbar_wait_bounded(sl_full(s), fill_par >> s & 1u, nullptr, kDrainLimitNs);
+                        if (leader) mbar_wait_bounded(ab_full(s), fill_par >> s & 1u, nullptr, kDrainLimitNs);
+                    }
+                if (*abort_flag) {
+                    const uint64_t t0 = globaltimer_ns();
+                    while (globaltimer_ns() - t0 < kPairAbortGraceNs) {
+                    }
+                }
             }
-            if (!ok) give_up();
-            // every MMA has completed (both CTAs' TMEM and shared memory) before the cluster tears down
-            umma_commit_pair_mc(drain_bar, 0x1);
-            mbar_wait_bounded(drain_bar, 0, nullptr, kDrainLimitNs);
+        } else if (warp == 1) {
+            // ---------------------------------------------------------------- MMA issuer (leader)
+            if (leader && lane == 0) {
+                int stage = 0;
+                uint32_t phase = 0, tphase = 0;
+                bool ok = true;
+                for (int64_t u = cluster_id; u < p.num_units && ok; u += num_clusters) {
+                    int tm, tn, s0, s1, split;
+                    fp4_unit(p, u, tm, tn, s0, s1, split);
+                    if (!mbar_wait_limit(tm_empty, tphase ^ 1u, abort_flag, kWaitLimitNs)) { ok = false; break; }
+                    for (int st = s0; st < s1; ++st) {
+                        if (!mbar_wait_limit(ab_full(stage), phase, abort_flag, kWaitLimitNs)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t sf = tmem_base + kF4Pair + (uint32_t)stage * kF4PairSfCols;
+                        const uint64_t wd = smem_desc_k_sw128(sbase + S::w_off + stage * kF4PairTile);
+                        const uint64_t td = smem_desc_k_sw128(sbase + S::t_off + stage * kF4PairTile);
+                        const int left = p.K - st * kF4PairStepK;
+                        // MMA k: 32 bytes further in the 128-byte rows, the second half after four; factor
+                        // bytes 0, 1 or 2, 3 of the words of chunk k / 2
+                        auto mma = [&](int k, uint32_t accum) {
+                            const uint64_t step = (uint64_t)((k & 3) * 2 + (k >> 2) * (int)(kF4PairHalf >> 4));
+                            const uint32_t id = (uint32_t)(k & 1) * 2u;
+                            const uint32_t col = (sf + (uint32_t)(k >> 1) * (kF4PairSfCols / 4)) | (id << 30);
+                            umma_f4_bs_pair(tmem_base, wd + step, td + step, idesc_e2m1_bs(kF4Pair, kF4Pair, id), col,
+                                            col + 4, accum);
+                        };
+                        if (left >= kF4PairStepK) {
+                            mma(0, st > s0 ? 1u : 0u);
+#pragma unroll
+                            for (int k = 1; k < 8; ++k) mma(k, 1u);
+                        } else {
+                            for (int k = 0; k * kF4MmaK < left; ++k) mma(k, (st > s0 || k > 0) ? 1u : 0u);
+                        }
+                        if (st + 1 == s1) umma_commit_pair_mc(tm_full, 0x3);
+                        umma_commit_pair_mc(ab_empty(stage), 0x3);
+                        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                    }
+                    tphase ^= 1u;
+                }
+                if (!ok) give_up();
+                // every MMA has completed (both CTAs' TMEM and shared memory) before the cluster tears down
+                umma_commit_pair_mc(drain_bar, 0x1);
+                mbar_wait_bounded(drain_bar, 0, nullptr, kDrainLimitNs);
+            }
         }
-    } else if (warp >= 4 && warp < 4 + kF4PairEpiWarps) {
+    } else if (warp < 4 + kF4PairEpiWarps) {
+        setmaxnreg_inc<kF4EpiRegs>();
         // ---------------------------------------------------------------- epilogue
         const int lq = warp & 3;
         const int col0 = ((warp - 4) >> 2) * 128;
@@ -238,53 +249,43 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
             tc_fence_after();
             const int n = tn * kF4Pair + (int)rank * 128 + lq * 32 + lane;
             const int m0 = tm * kF4Pair + col0;
-            auto release = [&]() {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (leader) mbar_arrive(tm_empty);
-                    else mbar_arrive_remote(mapa_shared(tm_empty, 0));
-                }
+            uint32_t r0[32], r1[32], r2[32], r3[32];
+            tmem_ld_32x32b_x32(taddr, r0);
+            tmem_ld_32x32b_x32(taddr + 32, r1);
+            tmem_ld_32x32b_x32(taddr + 64, r2);
+            tmem_ld_32x32b_x32(taddr + 96, r3);
+            tmem_ld_wait();
+            reg_after_wait32(r0);
+            reg_after_wait32(r1);
+            reg_after_wait32(r2);
+            reg_after_wait32(r3);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) mbar_arrive(tm_empty);
+                else mbar_arrive_remote(mapa_shared(tm_empty, 0));
+            }
+            auto val = [&](int c) -> float {
+                const uint32_t* rr = c < 32 ? r0 : c < 64 ? r1 : c < 96 ? r2 : r3;
+                return __uint_as_float(rr[c & 31]);
             };
-            if (p.out_f32) {
-                float* dst = static_cast<float*>(p.D) + (int64_t)m0 * p.ldd + n;
+            if (n < p.N) {
+                if (p.out_f32) {
+                    float* dst = static_cast<float*>(p.D) + (int64_t)m0 * p.ldd + n;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(taddr + 32 * i, r);
-                    tmem_ld_wait();
-                    reg_after_wait32(r);
-                    if (i == 3) release();
-                    if (n < p.N) {
+                    for (int c = 0; c < 128; ++c, dst += p.ldd)
+                        if (m0 + c < p.M) *dst = val(c);
+                } else {
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.D) + (int64_t)m0 * p.ldd + n;
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (m0 + 32 * i + c < p.M) dst[(32 * i + c) * p.ldd] = __uint_as_float(r[c]);
-                    }
-                }
-            } else {
-                // two columns (tokens) of the lane's row of B^T to a register
-                uint32_t w[64];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(taddr + 32 * i, r);
-                    tmem_ld_wait();
-                    reg_after_wait32(r);
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        w[16 * i + c] = cvt_bf16x2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
-                }
-                release();
-                if (n < p.N) {
-                    uint16_t* dst = static_cast<uint16_t*>(p.D) + (int64_t)m0 * p.ldd + n;
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (m0 + c < p.M) dst[c * p.ldd] = (uint16_t)(w[c >> 1] >> (16 * (c & 1)));
+                    for (int c = 0; c < 128; ++c, dst += p.ldd)
+                        if (m0 + c < p.M) *dst = __float2bfloat16_rn(val(c));
                 }
             }
         }
         if (!ok && lane == 0) give_up();
-    } else if (warp >= 4 + kF4PairEpiWarps) {
+    } else {
+        setmaxnreg_dec<kF4WriterRegs>();
         // ---------------------------------------------------------------- scale-factor writers
         const uint32_t taddr = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + kF4Pair;
         int stage = 0;

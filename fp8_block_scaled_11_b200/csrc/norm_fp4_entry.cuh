@@ -182,6 +182,11 @@ fp8bs_status launch_fp4_pair(DeviceInfo* d, const CUtensorMap& tW, const CUtenso
             if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Fp4PairSmem::alloc) !=
                 cudaSuccess)
                 return FP8BS_ERR_CUDA;
+            // the register hand-over is sized for this exact allocation at launch:
+            // with fewer the epilogue's increase could never be granted
+            cudaFuncAttributes fa;
+            if (cudaFuncGetAttributes(&fa, k) != cudaSuccess) return FP8BS_ERR_CUDA;
+            if (fa.numRegs != kF4LaunchRegs) return FP8BS_ERR_UNSUPPORTED;
             cfg.gridDim = dim3(2 * std::max(1, d->num_sms / 2), 1, 1);
             if (cudaOccupancyMaxActiveClusters(&nc, k, &cfg) != cudaSuccess) return FP8BS_ERR_CUDA;
             if (nc < 1) return FP8BS_ERR_UNSUPPORTED;
