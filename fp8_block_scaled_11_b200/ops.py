@@ -400,6 +400,73 @@ def fp8_scaled_gemm_quant(A: torch.Tensor, Bt: torch.Tensor, scale_a: torch.Tens
     return out, q_out, scale_out
 
 
+# ---------------------------------------------------------------------------- norm and 4-bit helpers
+# These calls are short on the GPU (a few microseconds for a token), so their
+# checks are written to cost little: one comparison per property.
+def _mat(t: torch.Tensor, shape, dtype, dev, what: str):
+    """Address and leading dimension of a row-major matrix of this shape, dtype and device."""
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{what}: expected {tuple(shape)} {dtype} on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    ld, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{what}: expected a row-major matrix (unit column stride)")
+    return t.data_ptr(), ld
+
+
+def _vec(t: torch.Tensor, n: int, dev, what: str) -> int:
+    """Address of a contiguous vector of n elements on this device."""
+    if t.dim() != 1 or t.numel() != n or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous vector of {n} elements on {dev}, got {tuple(t.shape)} on "
+                         f"{t.device}")
+    return t.data_ptr()
+
+
+def _vec32(t: torch.Tensor, n: int, dev, what: str) -> int:
+    if t.dtype != torch.float32:
+        raise ValueError(f"{what}: expected fp32, got {t.dtype}")
+    return _vec(t, n, dev, what)
+
+
+def _buffer(t: Optional[torch.Tensor], dev, what: str):
+    """Address and bytes of a scratch buffer (0, 0 for none)."""
+    if t is None:
+        return 0, 0
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous buffer on {dev}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _tiles(s: torch.Tensor, rows: int, cols: int, dev, what: str) -> int:
+    if (s.dtype != torch.uint8 or s.device != dev or not s.is_contiguous()
+            or s.numel() != (rows + 127) // 128 * ((cols + 127) // 128) * 512):
+        raise ValueError(f"{what}: expected the fp4_scale_tiles of a {rows} x {cols} matrix on {dev}")
+    return s.data_ptr()
+
+
+_DTYPE_CODES = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _code(t: torch.Tensor, what: str) -> int:
+    c = _DTYPE_CODES.get(t.dtype)
+    if c is None:
+        raise TypeError(f"{what}: unsupported dtype {t.dtype} (bf16 or fp32)")
+    return c
+
+
+def _call(fn: str, dev: torch.device, *args):
+    """Calls the C entry point on dev's current stream, with dev current."""
+    index = dev.index
+    if dev.type != "cuda":
+        raise ValueError(f"{fn}: expected CUDA tensors, got {dev}")
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            status = getattr(_lib or lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        status = getattr(_lib or lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != FP8BS_OK:
+        raise Fp8bsError(fn, status)
+
+
 # ---------------------------------------------------------------------------- microscaled 4 bits
 def fp4_scale_tiles(rows: int, cols: int, device) -> torch.Tensor:
     """Allocate the scale tiles of a rows x cols matrix of 4-bit codes: a uint8
@@ -408,26 +475,20 @@ def fp4_scale_tiles(rows: int, cols: int, device) -> torch.Tensor:
     return torch.empty(((rows + 127) // 128, (cols + 127) // 128, 32, 4, 4), dtype=torch.uint8, device=device)
 
 
+def _packed(rows: int, cols: int, device) -> torch.Tensor:
+    """rows x cols/2 bytes of packed codes whose rows start 16-byte aligned."""
+    return torch.empty((rows, _round_up(cols // 2, 16)), dtype=torch.uint8, device=device)[:, :cols // 2]
+
+
 def _codes(q: torch.Tensor, what: str):
-    """rows, codes per row and the leading dimension (bytes) of packed codes."""
+    """rows, codes per row, address and leading dimension (bytes) of packed codes."""
     if q.dtype != torch.uint8:
         raise TypeError(f"{what}: packed 4-bit codes are uint8")
-    return q.shape[0], 2 * q.shape[1], _ld(q)
-
-
-def _tiles(s: torch.Tensor, rows: int, cols: int, device, what: str) -> int:
-    if (s.dtype != torch.uint8 or s.device != device or not s.is_contiguous()
-            or s.numel() != (rows + 127) // 128 * ((cols + 127) // 128) * 512):
-        raise ValueError(f"{what}: expected the fp4_scale_tiles of a {rows} x {cols} matrix on {device}")
-    return s.data_ptr()
-
-
-def _on(t: torch.Tensor, device, what: str, shape=None, dtype=None) -> int:
-    """t's address, after its device, shape and dtype are checked."""
-    if t.device != device or (shape is not None and tuple(t.shape) != shape) or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{what}: expected {shape or 'a tensor'} {dtype or ''} on {device}, got {tuple(t.shape)} "
-                         f"{t.dtype} on {t.device}")
-    return t.data_ptr()
+    rows, half = q.shape
+    ld, one = q.stride()
+    if one != 1:
+        raise ValueError(f"{what}: expected a row-major matrix (unit column stride)")
+    return rows, 2 * half, q.data_ptr(), ld
 
 
 def fp4_quant_1x32(x: torch.Tensor, transpose_out: bool = False, q: Optional[torch.Tensor] = None,
@@ -437,29 +498,29 @@ def fp4_quant_1x32(x: torch.Tensor, transpose_out: bool = False, q: Optional[tor
     32 == 0).  transpose_out=True: groups along its rows (rows % 32 == 0); q is
     cols x rows/2.  Preallocated outputs may be passed as q / scale."""
     rows, cols = x.shape
-    xt = _dtype_code(x)
+    dev, xt = x.device, _code(x, "x")
+    xp, ldx = _mat(x, x.shape, x.dtype, dev, "x")
     R, C = (cols, rows) if transpose_out else (rows, cols)
     if q is None:
-        # rows of bytes start 16-byte aligned
-        q = torch.empty((R, _round_up(C // 2, 16)), dtype=torch.uint8, device=x.device)[:, :C // 2]
+        q = _packed(R, C, dev)
     if scale is None:
-        scale = fp4_scale_tiles(R, C, x.device)
-    _check("fp4_quant_1x32", lib().fp4_quant_1x32(x.data_ptr(), xt, rows, cols, _ld(x),
-                                                  _on(q, x.device, "q", (R, C // 2), torch.uint8), _ld(q),
-                                                  _tiles(scale, R, C, x.device, "scale"), int(transpose_out),
-                                                  _stream(x)))
+        scale = fp4_scale_tiles(R, C, dev)
+    qp, ldq = _mat(q, (R, C // 2), torch.uint8, dev, "q")
+    _call("fp4_quant_1x32", dev, xp, xt, rows, cols, ldx, qp, ldq, _tiles(scale, R, C, dev, "scale"),
+          int(transpose_out))
     return q, scale
 
 
 def fp4_dequant_1x32(q: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16,
                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of packed 4-bit codes and their scale tiles."""
-    rows, cols, ldq = _codes(q, "q")
+    rows, cols, qp, ldq = _codes(q, "q")
+    dev = q.device
     if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype, device=q.device)
-    _check("fp4_dequant_1x32", lib().fp4_dequant_1x32(q.data_ptr(), ldq, _tiles(scale, rows, cols, q.device, "scale"),
-                                                      rows, cols, _on(out, q.device, "out", (rows, cols)),
-                                                      _dtype_code(out), _ld(out), _stream(q)))
+        out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+    op, ldo = _mat(out, (rows, cols), out.dtype, dev, "out")
+    _call("fp4_dequant_1x32", dev, qp, ldq, _tiles(scale, rows, cols, dev, "scale"), rows, cols, op,
+          _code(out, "out"), ldo)
     return out
 
 
@@ -475,22 +536,20 @@ def fp4_scaled_gemm(A: torch.Tensor, Bt: torch.Tensor, scale_a: torch.Tensor, sc
     """D = A . Bt^T of two microscaled 4-bit matrices: A M x K/2 and Bt N x K/2
     uint8 (two codes a byte) with their scale tiles, as fp4_quant_1x32 returns
     them.  D: M x N, bf16 or fp32."""
-    M, K, lda = _codes(A, "A")
-    N, K2, ldb = _codes(Bt, "Bt")
-    if K2 != K:
-        raise ValueError("A and Bt must share K")
+    M, K, ap, lda = _codes(A, "A")
+    N, K2, bp, ldb = _codes(Bt, "Bt")
     dev = A.device
+    if K2 != K or Bt.device != dev:
+        raise ValueError("A and Bt must share K and the device")
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    dp, ldd = _mat(out, (M, N), out.dtype, dev, "out")
+    oc = _code(out, "out")
     if split_k and workspace is None:
         workspace = fp4_scaled_gemm_workspace(M, N, K, dev)
-    wp, wn = ((_on(workspace, dev, "workspace"), workspace.numel() * workspace.element_size())
-              if split_k and workspace is not None else (0, 0))
-    _check("fp4_scaled_gemm", lib().fp4_scaled_gemm(M, N, K, A.data_ptr(), lda, _on(Bt, dev, "Bt"), ldb,
-                                                    _tiles(scale_a, M, K, dev, "scale_a"),
-                                                    _tiles(scale_b, N, K, dev, "scale_b"),
-                                                    _on(out, dev, "out", (M, N)), _ld(out), _dtype_code(out), wp, wn,
-                                                    _stream(A)))
+    wp, wn = _buffer(workspace if split_k else None, dev, "workspace")
+    _call("fp4_scaled_gemm", dev, M, N, K, ap, lda, bp, ldb, _tiles(scale_a, M, K, dev, "scale_a"),
+          _tiles(scale_b, N, K, dev, "scale_b"), dp, ldd, oc, wp, wn)
     return out
 
 
@@ -502,37 +561,32 @@ def rmsnorm_quant_buffers(x: torch.Tensor, residual: bool = False, want_y: bool 
     rows, cols = x.shape
     dev = x.device
     if bits == 8:
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-        s = colmajor_grid(rows, (cols + 127) // 128, dev)
+        q, s = (torch.empty((rows, cols), dtype=torch.uint8, device=dev),
+                colmajor_grid(rows, (cols + 127) // 128, dev))
+    elif bits == 4:
+        q, s = _packed(rows, cols, dev), fp4_scale_tiles(rows, cols, dev)
     else:
-        q = torch.empty((rows, _round_up(cols // 2, 16)), dtype=torch.uint8, device=dev)[:, :cols // 2]
-        s = fp4_scale_tiles(rows, cols, dev)
-    new = lambda: torch.empty((rows, cols), dtype=x.dtype, device=dev)  # noqa: E731
-    return (q, s, new() if residual else None, torch.empty((rows,), dtype=torch.float32, device=dev),
-            new() if want_y else None)
+        raise ValueError("bits is 8 or 4")
+    return (q, s, torch.empty((rows, cols), dtype=x.dtype, device=dev) if residual else None,
+            torch.empty((rows,), dtype=torch.float32, device=dev),
+            torch.empty((rows, cols), dtype=x.dtype, device=dev) if want_y else None)
 
 
-def _rmsnorm_quant(fn, bits, x, weight, residual, eps, want_y, out, tail):
-    rows, cols = x.shape
-    xt, dev = _dtype_code(x), x.device
-    if out is None:
-        out = rmsnorm_quant_buffers(x, residual is not None, want_y, bits)
-    q, s, h, rstd, y = out
+def _norm_args(x, weight, residual, out, eps, bits):
+    """The arguments both forward entry points share, from x to the leading dimension of q."""
+    shape, dt, dev = x.shape, x.dtype, x.device
+    rows, cols = shape
+    q, _, h, rstd, y = out
+    xt = _code(x, "x")
+    xp, ldx = _mat(x, shape, dt, dev, "x")
     if (h is None) != (residual is None):
-        raise ValueError(f"{fn}: out has h exactly where there is a residual")
-    shape, dt = (rows, cols), x.dtype
-    rp = lr = hp = lh = yp = ly = 0
-    if residual is not None:
-        rp, lr = _on(residual, dev, "residual", shape, dt), _ld(residual)
-        hp, lh = _on(h, dev, "h", shape, dt), _ld(h)
-    if y is not None:
-        yp, ly = _on(y, dev, "y", shape, dt), _ld(y)
-    if not weight.is_contiguous() or not rstd.is_contiguous():
-        raise ValueError(f"{fn}: weight and rstd must be contiguous")
-    _check(fn, getattr(lib(), fn)(x.data_ptr(), _ld(x), rp, lr, xt, rows, cols, _on(weight, dev, "weight", (cols,)),
-                                  _dtype_code(weight), eps, hp, lh, _on(rstd, dev, "rstd", (rows,), torch.float32), yp,
-                                  ly, _on(q, dev, "q", (rows, cols * bits // 8), torch.uint8), _ld(q), *tail(s)))
-    return q, s, x if residual is None else h, rstd, y
+        raise ValueError("out has h exactly where there is a residual")
+    rp, ldr = (0, 0) if residual is None else _mat(residual, shape, dt, dev, "residual")
+    hp, ldh = (0, 0) if h is None else _mat(h, shape, dt, dev, "h")
+    yp, ldy = (0, 0) if y is None else _mat(y, shape, dt, dev, "y")
+    qp, ldq = _mat(q, (rows, cols * bits // 8), torch.uint8, dev, "q")
+    return (xp, ldx, rp, ldr, xt, rows, cols, _vec(weight, cols, dev, "weight"), _code(weight, "weight"), eps, hp, ldh,
+            _vec32(rstd, rows, dev, "rstd"), yp, ldy, qp, ldq)
 
 
 def fp8_rmsnorm_quant_1x128(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -541,21 +595,27 @@ def fp8_rmsnorm_quant_1x128(x: torch.Tensor, weight: torch.Tensor, residual: Opt
     returns (q, scale_inv grid, h, rstd, y); h is x without a residual, y (the
     norm's value in x's dtype) None unless want_y.  Preallocated outputs may be
     passed as out (rmsnorm_quant_buffers); h may be x or residual itself."""
-    dev = x.device
-
-    def tail(s):
-        return (_on(s, dev, "scale_inv", (x.shape[0], (x.shape[1] + 127) // 128), torch.float32),
-                _grid_ld(s, x.shape[0]), int(rule), _stream(x))
-    return _rmsnorm_quant("fp8_rmsnorm_quant_1x128", 8, x, weight, residual, eps, want_y, out, tail)
+    if out is None:
+        out = rmsnorm_quant_buffers(x, residual is not None, want_y)
+    args = _norm_args(x, weight, residual, out, eps, 8)
+    q, s, h, rstd, y = out
+    rows, cols = x.shape
+    if s.shape != (rows, (cols + 127) // 128) or s.device != x.device:
+        raise ValueError(f"scale_inv: expected a ({rows}, {(cols + 127) // 128}) grid on {x.device}")
+    _call("fp8_rmsnorm_quant_1x128", x.device, *args, s.data_ptr(), _grid_ld(s, rows), rule)
+    return q, s, x if residual is None else h, rstd, y
 
 
 def fp4_rmsnorm_quant_1x32(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
                            eps: float = 1e-6, want_y: bool = False, out=None):
     """fp8_rmsnorm_quant_1x128 with its result in microscaled 4 bits: q is rows x
     cols/2 packed codes, the scales are scale tiles (bits=4 buffers)."""
-    def tail(s):
-        return _tiles(s, x.shape[0], x.shape[1], x.device, "scale"), _stream(x)
-    return _rmsnorm_quant("fp4_rmsnorm_quant_1x32", 4, x, weight, residual, eps, want_y, out, tail)
+    if out is None:
+        out = rmsnorm_quant_buffers(x, residual is not None, want_y, 4)
+    args = _norm_args(x, weight, residual, out, eps, 4)
+    q, s, h, rstd, y = out
+    _call("fp4_rmsnorm_quant_1x32", x.device, *args, _tiles(s, x.shape[0], x.shape[1], x.device, "scale"))
+    return q, s, x if residual is None else h, rstd, y
 
 
 def rmsnorm_backward_workspace(h: torch.Tensor) -> torch.Tensor:
@@ -570,24 +630,20 @@ def fp8bs_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     y), the forward pass's h and rstd, and dh (the gradient that reaches h past
     the norm; added to dx).  Preallocated outputs may be passed as out=(dx,
     dweight); dx may be dy, dh or h itself."""
-    rows, cols = h.shape
-    xt, dev = _dtype_code(h), h.device
-    shape, dt = (rows, cols), h.dtype
+    shape, dt, dev = h.shape, h.dtype, h.device
+    rows, cols = shape
+    xt = _code(h, "h")
+    hp, ldh = _mat(h, shape, dt, dev, "h")
+    yp, ldy = _mat(dy, shape, dt, dev, "dy")
+    gp, ldg = (0, 0) if dh is None else _mat(dh, shape, dt, dev, "dh")
     dx, dw = out if out is not None else (torch.empty(shape, dtype=dt, device=dev),
                                           torch.empty((cols,), dtype=torch.float32, device=dev))
+    xp, ldx = _mat(dx, shape, dt, dev, "dx")
     if workspace is None:
         workspace = rmsnorm_backward_workspace(h)
-    gp, lg = (_on(dh, dev, "dh", shape, dt), _ld(dh)) if dh is not None else (0, 0)
-    if not (weight.is_contiguous() and rstd.is_contiguous() and dw.is_contiguous()):
-        raise ValueError("fp8bs_rmsnorm_backward: weight, rstd and dweight must be contiguous")
-    _check("fp8bs_rmsnorm_backward",
-           lib().fp8bs_rmsnorm_backward(_on(dy, dev, "dy", shape, dt), _ld(dy), h.data_ptr(), _ld(h), gp, lg, xt, rows,
-                                        cols, _on(weight, dev, "weight", (cols,)), _dtype_code(weight),
-                                        _on(rstd, dev, "rstd", (rows,), torch.float32),
-                                        _on(dx, dev, "dx", shape, dt), _ld(dx),
-                                        _on(dw, dev, "dweight", (cols,), torch.float32),
-                                        _on(workspace, dev, "workspace"),
-                                        workspace.numel() * workspace.element_size(), _stream(h)))
+    _call("fp8bs_rmsnorm_backward", dev, yp, ldy, hp, ldh, gp, ldg, xt, rows, cols, _vec(weight, cols, dev, "weight"),
+          _code(weight, "weight"), _vec32(rstd, rows, dev, "rstd"), xp, ldx, _vec32(dw, cols, dev, "dweight"),
+          *_buffer(workspace, dev, "workspace"))
     return dx, dw
 
 
