@@ -151,13 +151,13 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
                 int stage = 0;
                 uint32_t phase = 0;
                 for (int64_t u = cluster_id; u < p.num_units && ok; u += num_clusters) {
-                    int tm, tn, s0, s1, split;
-                    fp4_unit(p, u, tm, tn, s0, s1, split);
+                    int tm, tn, split;
+                    fp4_unit(p, (uint32_t)u, tm, tn, split);
                     const int tile = wside ? tn : tm;
                     const int row0 = tile * kF4Pair + (int)rank * 128;     // this CTA's rows of the operand
                     // scale tiles: of this CTA's rows of B^T, of all the tile's rows of A
                     const int block = wside ? row0 >> 7 : tile * 2;
-                    for (int st = s0; st < s1; ++st) {
+                    for (int st = 0; st < p.steps; ++st) {
                         if (!mbar_wait_limit(ab_empty(stage), phase ^ 1u, abort_flag, kWaitLimitNs)) { ok = false; break; }
                         if (leader) mbar_arrive_expect_tx(ab_full(stage), 2 * kF4PairTile);
                         mbar_arrive_expect_tx(sl_full(stage), sf_bytes);
@@ -193,10 +193,10 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
                 uint32_t phase = 0, tphase = 0;
                 bool ok = true;
                 for (int64_t u = cluster_id; u < p.num_units && ok; u += num_clusters) {
-                    int tm, tn, s0, s1, split;
-                    fp4_unit(p, u, tm, tn, s0, s1, split);
+                    int tm, tn, split;
+                    fp4_unit(p, (uint32_t)u, tm, tn, split);
                     if (!mbar_wait_limit(tm_empty, tphase ^ 1u, abort_flag, kWaitLimitNs)) { ok = false; break; }
-                    for (int st = s0; st < s1; ++st) {
+                    for (int st = 0; st < p.steps; ++st) {
                         if (!mbar_wait_limit(ab_full(stage), phase, abort_flag, kWaitLimitNs)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t sf = tmem_base + kF4Pair + (uint32_t)stage * kF4PairSfCols;
@@ -213,13 +213,13 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
                                             col + 4, accum);
                         };
                         if (left >= kF4PairStepK) {
-                            mma(0, st > s0 ? 1u : 0u);
+                            mma(0, st > 0 ? 1u : 0u);
 #pragma unroll
                             for (int k = 1; k < 8; ++k) mma(k, 1u);
                         } else {
-                            for (int k = 0; k * kF4MmaK < left; ++k) mma(k, (st > s0 || k > 0) ? 1u : 0u);
+                            for (int k = 0; k * kF4MmaK < left; ++k) mma(k, (st > 0 || k > 0) ? 1u : 0u);
                         }
-                        if (st + 1 == s1) umma_commit_pair_mc(tm_full, 0x3);
+                        if (st + 1 == p.steps) umma_commit_pair_mc(tm_full, 0x3);
                         umma_commit_pair_mc(ab_empty(stage), 0x3);
                         if (++stage == kStages) { stage = 0; phase ^= 1u; }
                     }
@@ -240,8 +240,8 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
         uint32_t tphase = 0;
         bool ok = true;
         for (int64_t u = cluster_id; u < p.num_units; u += num_clusters) {
-            int tm, tn, s0, s1, split;
-            fp4_unit(p, u, tm, tn, s0, s1, split);
+            int tm, tn, split;
+            fp4_unit(p, (uint32_t)u, tm, tn, split);
             if (!mbar_wait_limit(tm_full, tphase, abort_flag, kWaitLimitNs)) ok = false;
             tphase ^= 1u;
             ok = __all_sync(0xffffffffu, ok);
@@ -292,9 +292,9 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
         uint32_t phase = 0;
         bool ok = true;
         for (int64_t u = cluster_id; u < p.num_units && ok; u += num_clusters) {
-            int tm, tn, s0, s1, split;
-            fp4_unit(p, u, tm, tn, s0, s1, split);
-            for (int st = s0; st < s1; ++st) {
+            int tm, tn, split;
+            fp4_unit(p, (uint32_t)u, tm, tn, split);
+            for (int st = 0; st < p.steps; ++st) {
                 if (!mbar_wait_limit(sl_full(stage), phase, abort_flag, kWaitLimitNs)) ok = false;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;

@@ -103,7 +103,9 @@ fp8bs_status launch_norm_back(const BackPlan& b, const NormBackParams& p, float*
 struct Fp4Plan {
     bool pair;                  // 256 x 256 tiles on CTA pairs; else 128 x bn tiles on single CTAs
     int bn;
-    int tiles_m, tiles_n, splits;
+    int tiles_m, tiles_n;
+    int max_parts;              // CTAs of a cluster that may share a tile's K
+    int splits;                 // parts of K that go through the workspace
     int64_t ldw;
     size_t ws_bytes;
 };
@@ -113,16 +115,22 @@ Fp4Plan plan_fp4(int64_t M, int64_t N, int64_t K, int num_sms)
     Fp4Plan s;
     s.pair = M > 128 && cdiv(N, kF4Pair) * cdiv(M, kF4Pair) >= num_sms / 2;
     s.tiles_n = (int)cdiv(N, s.pair ? kF4Pair : kF4Rows);
-    // single CTAs: the narrowest tile that holds every token
-    s.bn = s.pair ? kF4Pair : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    // single CTAs: the narrowest tile that holds every token, and 128 columns only
+    // where the tiles fill the SMs without K being split
+    s.bn = s.pair ? kF4Pair : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 || s.tiles_n * cdiv(M, 128) < num_sms ? 64 : 128;
     s.tiles_m = (int)cdiv(M, s.bn);
-    const int64_t tiles = (int64_t)s.tiles_m * s.tiles_n;
-    const int64_t steps = cdiv(K, kF4StepK);
+    s.max_parts = 1;
     int splits = 1;
-    if (!s.pair && tiles * 2 <= num_sms) {
-        // fill the SMs, with at least four steps (16 KB of weights each) per split
-        splits = (int)std::min<int64_t>(num_sms / tiles, std::max<int64_t>(1, steps / 4));
-        splits = std::max(1, std::min(splits, 64));
+    if (s.bn <= 64) {
+        // K over the CTAs of a cluster: as many as two CTAs per SM have room for,
+        // with at least two steps each
+        const int64_t tiles = (int64_t)s.tiles_m * s.tiles_n;
+        const int64_t steps = cdiv(K, kF4StepK);
+        const int64_t room = std::max<int64_t>(1, std::min(2 * num_sms / tiles, steps / 2));
+        s.max_parts = (int)std::min<int64_t>(room, kF4MaxCluster);
+        // and over clusters, where that leaves more than half of the room and 8 steps each
+        if (room >= 2 * kF4MaxCluster)
+            splits = (int)std::max<int64_t>(1, std::min<int64_t>({room / kF4MaxCluster, steps / (8 * kF4MaxCluster), 32}));
     }
     s.splits = splits;
     s.ldw = (N + 3) & ~int64_t(3);
@@ -131,22 +139,50 @@ Fp4Plan plan_fp4(int64_t M, int64_t N, int64_t K, int num_sms)
 }
 
 template <int BN>
-fp8bs_status launch_fp4(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap& tT, const Fp4Params& p,
+fp8bs_status launch_fp4(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap& tT, const Fp4Params& p, int max_parts,
                         cudaStream_t stream)
 {
     auto k = gemm_fp4_kernel<BN>;
     constexpr int slot = BN == 16 ? 0 : BN == 32 ? 1 : BN == 64 ? 2 : 3;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kF4Threads, 1, 1);
+    cfg.dynamicSmemBytes = Fp4Cfg<BN>::alloc;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     if (!d->fp4_attr_set[slot].load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> lock(g_mutex);
         if (!d->fp4_attr_set[slot].load(std::memory_order_relaxed)) {
             if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Fp4Cfg<BN>::alloc) !=
                 cudaSuccess)
                 return FP8BS_ERR_CUDA;
+            // clusters of 2, 4 and 8 CTAs that can be resident at once: the GPU's
+            // processor groups need not hold a whole number of them
+            for (int i = 1; Fp4Cfg<BN>::split && i <= 3; ++i) {
+                attr[0].val.clusterDim.x = 1u << i;
+                cfg.gridDim = dim3((unsigned)(2 * d->num_sms >> i << i), 1, 1);
+                int nc = 0;
+                if (cudaOccupancyMaxActiveClusters(&nc, k, &cfg) != cudaSuccess) return FP8BS_ERR_CUDA;
+                d->fp4_clusters[slot][i].store(nc, std::memory_order_relaxed);
+            }
             d->fp4_attr_set[slot].store(true, std::memory_order_release);
         }
     }
-    const int grid = (int)std::min<int64_t>(p.num_units, d->num_sms);
-    k<<<grid, Fp4Cfg<BN>::threads, Fp4Cfg<BN>::alloc, stream>>>(tW, tT, p);
+    // the most CTAs per tile with which all clusters are resident at once
+    int log_parts = 0;
+    for (int i = 1; i <= 3; ++i)
+        if ((1 << i) <= max_parts && p.num_units <= d->fp4_clusters[slot][i].load(std::memory_order_relaxed)) log_parts = i;
+    attr[0].val.clusterDim.x = 1u << log_parts;
+    cfg.gridDim = dim3((unsigned)(p.num_units << log_parts), 1, 1);
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, k, tW, tT, p) != cudaSuccess) return FP8BS_ERR_CUDA;
     return launch_status();
 }
 
@@ -411,10 +447,10 @@ fp8bs_status fp4_scaled_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* A, 
     p.err = d->err_ptr;
     if (plan.pair) return launch_fp4_pair(d, tW, tT, p, stream);
     switch (plan.bn) {
-    case 16: st = launch_fp4<16>(d, tW, tT, p, stream); break;
-    case 32: st = launch_fp4<32>(d, tW, tT, p, stream); break;
-    case 64: st = launch_fp4<64>(d, tW, tT, p, stream); break;
-    default: st = launch_fp4<128>(d, tW, tT, p, stream); break;
+    case 16: st = launch_fp4<16>(d, tW, tT, p, plan.max_parts, stream); break;
+    case 32: st = launch_fp4<32>(d, tW, tT, p, plan.max_parts, stream); break;
+    case 64: st = launch_fp4<64>(d, tW, tT, p, plan.max_parts, stream); break;
+    default: st = launch_fp4<128>(d, tW, tT, p, plan.max_parts, stream); break;
     }
     if (st != FP8BS_OK || plan.splits == 1) return st;
     const int vec_out = aligned16(D) && (ldd * (int64_t)dtype_size(out_dtype)) % 16 == 0;

@@ -71,6 +71,33 @@ __device__ __forceinline__ void tmem_st_wait()
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ uint32_t cluster_nctarank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+// The two halves of cluster_sync_all: work between them runs while the peers
+// arrive.  Every thread of the CTA executes both.
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// 16 bytes into a cluster CTA's shared memory, counted on an mbarrier of the
+// same CTA (both shared::cluster addresses).
+__device__ __forceinline__ void st_async_v4(uint32_t cluster_addr, const uint32_t* r, uint32_t cluster_bar)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+                 ::"r"(cluster_addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(cluster_bar)
+                 : "memory");
+}
+
 // mbar_wait_bounded that looks at the clock only every 64 tries (each try waits
 // inside the instruction for a while): the tries that find the phase complete,
 // nearly all of them, read no timer.
