@@ -114,6 +114,11 @@ __device__ __forceinline__ void fp4_unit(const Fp4Params& p, uint32_t u, int& tm
         tile = u / (uint32_t)p.splits;
         split = (int)(u - tile * (uint32_t)p.splits);
     }
+    if (p.tiles_m == 1) {
+        tm = 0;
+        tn = (int)tile;
+        return;
+    }
     const uint32_t per_band = (uint32_t)(p.band * p.tiles_m);
     const uint32_t band = tile / per_band;
     const uint32_t in = tile - band * per_band;
@@ -123,12 +128,72 @@ __device__ __forceinline__ void fp4_unit(const Fp4Params& p, uint32_t u, int& tm
     tn = n0 + (int)(in - (uint32_t)tm * width);
 }
 
-// One element of D, or of the workspace's part `split`.
-__device__ __forceinline__ void fp4_store(const Fp4Params& p, int split, int m, int n, float v)
+// `cnt` (at most CNT) consecutive columns of D^T, i.e. one element in each of
+// that many rows of D, ld elements apart.
+template <int CNT>
+__device__ __forceinline__ void fp4_store(float* dst, int64_t ld, const float (&v)[CNT], int cnt)
 {
-    if (p.splits > 1) p.ws[((int64_t)split * p.M + m) * p.ldw + n] = v;
-    else if (p.out_f32) static_cast<float*>(p.D)[(int64_t)m * p.ldd + n] = v;
-    else static_cast<__nv_bfloat16*>(p.D)[(int64_t)m * p.ldd + n] = __float2bfloat16_rn(v);
+    if (cnt >= CNT) {
+#pragma unroll
+        for (int c = 0; c < CNT; ++c, dst += ld) *dst = v[c];
+    } else {
+#pragma unroll
+        for (int c = 0; c < CNT; ++c, dst += ld)
+            if (c < cnt) *dst = v[c];
+    }
+}
+template <int CNT>
+__device__ __forceinline__ void fp4_store(__nv_bfloat16* dst, int64_t ld, const float (&v)[CNT], int cnt)
+{
+    if (cnt >= CNT) {
+#pragma unroll
+        for (int c = 0; c < CNT; ++c, dst += ld) *dst = __float2bfloat16_rn(v[c]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < CNT; ++c, dst += ld)
+            if (c < cnt) *dst = __float2bfloat16_rn(v[c]);
+    }
+}
+
+// A tile's accumulator (or, with K split over a cluster, this CTA's quads of it)
+// to D or to the workspace.  `dst`: row m0, the lane's column.
+template <int BN, typename T>
+__device__ __forceinline__ void fp4_store_tile(uint32_t taddr, T* dst, int64_t ld, int cols, bool store)
+{
+    constexpr int kChunk = BN < 32 ? 16 : 32;
+#pragma unroll 1
+    for (int c0 = 0; c0 < cols; c0 += kChunk) {
+        uint32_t r[kChunk / 16][16];
+#pragma unroll
+        for (int i = 0; i < kChunk / 16; ++i) tmem_ld_32x32b_x16(taddr + (uint32_t)(c0 + 16 * i), r[i]);
+        tmem_ld_wait(r[0]);
+#pragma unroll
+        for (int i = 1; i < kChunk / 16; ++i) reg_after_wait(r[i]);
+        if (store) {
+            float v[kChunk];
+#pragma unroll
+            for (int c = 0; c < kChunk; ++c) v[c] = __uint_as_float(r[c >> 4][c & 15]);
+            fp4_store(dst + (int64_t)c0 * ld, ld, v, cols - c0);
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void fp4_store_quads(uint32_t mine, uint32_t share, uint32_t parts, uint32_t rank,
+                                                uint32_t owned, T* dst, int64_t ld, int cols)
+{
+#pragma unroll 2
+    for (uint32_t g = 0; g < owned; ++g) {
+        float4 v[kF4MaxCluster];
+#pragma unroll
+        for (int j = 0; j < kF4MaxCluster; ++j)
+            if (j < (int)parts) v[j] = lds128(mine + (uint32_t)j * share + g * kQuadBytes);
+        float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+        for (int j = 1; j < kF4MaxCluster; ++j)
+            if (j < (int)parts) { sum[0] += v[j].x; sum[1] += v[j].y; sum[2] += v[j].z; sum[3] += v[j].w; }
+        const int c = (int)(g * parts + rank) * 4;
+        fp4_store(dst + (int64_t)c * ld, ld, sum, cols - c);
+    }
 }
 
 template <int BN>
@@ -151,12 +216,13 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const uint32_t rank = cluster_ctarank(), parts = cluster_nctarank();
 
     int tm, tn, split;
-    fp4_unit(p, blockIdx.x / parts, tm, tn, split);
+    const int log_parts = 31 - __clz((int)parts);
+    fp4_unit(p, blockIdx.x >> log_parts, tm, tn, split);
     const int m0 = tm * BN, n0 = tn * kF4Rows;
     const int cols = min(BN, p.M - m0);                 // columns (tokens) that D has
     const uint32_t quads = (uint32_t)(cols + 3) >> 2;
     // of which this CTA owns quads rank, rank + parts, ..
-    const uint32_t owned = quads > rank ? (quads - rank + parts - 1) / parts : 0;
+    const uint32_t owned = quads > rank ? (quads - rank + parts - 1) >> log_parts : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::stages; ++s) {
@@ -182,9 +248,14 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     // the peers may send once every CTA of the cluster has passed here
     if (C::split && parts > 1) cluster_arrive();
     const uint32_t tmem_base = *tmem_slot;
-    const uint32_t part = (uint32_t)split * parts + rank, all = (uint32_t)p.splits * parts;
-    // (steps <= 2^23, all <= 256: 32 bits hold the products)
-    const int s0 = (int)((uint32_t)p.steps * part / all), s1 = (int)((uint32_t)p.steps * (part + 1) / all);
+    // this CTA's steps: part of p.splits * parts (steps <= 2^23 and at most 256
+    // parts: 32 bits hold the products)
+    uint32_t s0 = (uint32_t)p.steps * ((uint32_t)split * parts + rank) >> log_parts;
+    uint32_t s1 = (uint32_t)p.steps * ((uint32_t)split * parts + rank + 1) >> log_parts;
+    if (p.splits > 1) {
+        s0 /= (uint32_t)p.splits;
+        s1 /= (uint32_t)p.splits;
+    }
     // everything above may run under the previous kernel's tail; the next one's
     // may run under this
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -202,7 +273,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             uint32_t phase = 0;
             bool ok = true;
             uint32_t filled = 0, fill_par = 0;
-            for (int st = s0; st < s1; ++st) {
+            for (int st = (int)s0; st < (int)s1; ++st) {
                 if (!mbar_wait_limit(ab_empty(stage), phase ^ 1u, abort_flag, kWaitLimitNs)) { ok = false; break; }
                 const uint32_t bytes = kSfTileBytes * (uint32_t)min(2, p.kcs - 2 * st);
                 mbar_arrive_expect_tx(sl_full(stage), 2 * bytes);
@@ -231,7 +302,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int st = s0; st < s1; ++st) {
+            for (int st = (int)s0; st < (int)s1; ++st) {
                 if (!mbar_wait_limit(ab_full(stage), phase, abort_flag, kWaitLimitNs)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t sf = tmem_base + C::acc_cols + (uint32_t)stage * C::sf_cols;
@@ -244,7 +315,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                     const uint32_t col = (sf + (uint32_t)(k >> 1) * (C::sf_cols / 2)) | (id << 30);
                     if (k * kF4MmaK < left)
                         umma_f4_bs(tmem_base, wd + 2 * k, td + 2 * k, idesc_e2m1_bs(kF4Rows, BN, id), col, col + 4,
-                                   (st > s0 || k > 0) ? 1u : 0u);
+                                   (st > (int)s0 || k > 0) ? 1u : 0u);
                 }
                 umma_commit(ab_empty(stage));
                 if (++stage == C::stages) { stage = 0; phase ^= 1u; }
@@ -261,7 +332,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int st = s0; st < s1; ++st) {
+        for (int st = (int)s0; st < (int)s1; ++st) {
             if (!mbar_wait_limit(sl_full(stage), phase, abort_flag, kWaitLimitNs)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -300,11 +371,16 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         if (!ok && lane == 0) give_up();
         tc_fence_after();
         const int row = lq * 32 + lane, n = n0 + row;
+        const bool bf16 = p.splits == 1 && !p.out_f32;
+        const int64_t ld = p.splits > 1 ? p.ldw : p.ldd;
+        float* dst32 = p.splits > 1 ? p.ws + ((int64_t)split * p.M + m0) * ld + n
+                                    : static_cast<float*>(p.D) + (int64_t)m0 * ld + n;
+        __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(p.D) + (int64_t)m0 * ld + n;
         if (C::split && parts > 1) {
             cluster_wait();
             // slot of (rank, owned quad i): 128 rows of 16 bytes
             const uint32_t mine = sbase + C::red_off + (uint32_t)row * 16u;
-            const uint32_t share = ((quads + parts - 1) / parts) * kQuadBytes;
+            const uint32_t share = ((quads + parts - 1) >> log_parts) * kQuadBytes;
             if (ok) {
                 uint32_t owner = 0, i = 0;
 #pragma unroll 1
@@ -327,35 +403,13 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             // gave up stays as well until what its peers send it has arrived
             if (owned > 0 && !mbar_wait_limit(red_full, 0, nullptr, 3 * kWaitLimitNs)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
-            for (uint32_t g = 0; ok && g < owned; ++g) {
-                float4 v[kF4MaxCluster];
-#pragma unroll
-                for (int j = 0; j < kF4MaxCluster; ++j)
-                    if (j < (int)parts) v[j] = lds128(mine + (uint32_t)j * share + g * kQuadBytes);
-                float4 sum = v[0];
-#pragma unroll
-                for (int j = 1; j < kF4MaxCluster; ++j)
-                    if (j < (int)parts) { sum.x += v[j].x; sum.y += v[j].y; sum.z += v[j].z; sum.w += v[j].w; }
-                const int c = (int)(g * parts + rank) * 4;
-                if (n < p.N) {
-                    fp4_store(p, split, m0 + c, n, sum.x);
-                    if (c + 1 < cols) fp4_store(p, split, m0 + c + 1, n, sum.y);
-                    if (c + 2 < cols) fp4_store(p, split, m0 + c + 2, n, sum.z);
-                    if (c + 3 < cols) fp4_store(p, split, m0 + c + 3, n, sum.w);
-                }
+            if (ok && n < p.N) {
+                if (bf16) fp4_store_quads(mine, share, parts, rank, owned, dst16, ld, cols);
+                else fp4_store_quads(mine, share, parts, rank, owned, dst32, ld, cols);
             }
         } else if (ok) {
-#pragma unroll 1
-            for (int c0 = 0; c0 < cols; c0 += 16) {
-                uint32_t r[16];
-                tmem_ld_32x32b_x16(lane_addr + (uint32_t)c0, r);
-                tmem_ld_wait(r);
-                if (n < p.N) {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        if (c0 + c < cols) fp4_store(p, split, m0 + c0 + c, n, __uint_as_float(r[c]));
-                }
-            }
+            if (bf16) fp4_store_tile<BN>(lane_addr, dst16, ld, cols, n < p.N);
+            else fp4_store_tile<BN>(lane_addr, dst32, ld, cols, n < p.N);
         }
         if (!ok && lane == 0) give_up();
     }

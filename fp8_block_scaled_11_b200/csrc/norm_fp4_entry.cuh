@@ -123,10 +123,12 @@ Fp4Plan plan_fp4(int64_t M, int64_t N, int64_t K, int num_sms)
     int splits = 1;
     if (s.bn <= 64) {
         // K over the CTAs of a cluster: as many as two CTAs per SM have room for,
-        // with at least two steps each
+        // with steps enough each (256 K, about 550 cycles) to pay for sending and
+        // adding the sums (600 cycles at 16 columns, 2300 at 64: at 777 x 1000 x
+        // 2080, nine steps in all, 6.0 us on one CTA per tile and 7.3 on two)
         const int64_t tiles = (int64_t)s.tiles_m * s.tiles_n;
         const int64_t steps = cdiv(K, kF4StepK);
-        const int64_t room = std::max<int64_t>(1, std::min(2 * num_sms / tiles, steps / 2));
+        const int64_t room = std::max<int64_t>(1, std::min<int64_t>(2 * num_sms / tiles, steps / (1 + s.bn / 16)));
         s.max_parts = (int)std::min<int64_t>(room, kF4MaxCluster);
         // and over clusters, where that leaves more than half of the room and 8 steps each
         if (room >= 2 * kF4MaxCluster)
@@ -163,14 +165,21 @@ fp8bs_status launch_fp4(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap&
             if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Fp4Cfg<BN>::alloc) !=
                 cudaSuccess)
                 return FP8BS_ERR_CUDA;
+            // two CTAs per SM need more than the default share of shared memory
+            if (cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+                cudaSuccess)
+                return FP8BS_ERR_CUDA;
             // clusters of 2, 4 and 8 CTAs that can be resident at once: the GPU's
-            // processor groups need not hold a whole number of them
+            // processor groups need not hold a whole number of them.  The query
+            // counts one CTA per SM; two fit by Fp4Cfg's limits on registers,
+            // shared memory and TMEM (256 CTAs in clusters of four, 24 x 8192 x
+            // 5120: 5.5 us, on half as many 6.5).
             for (int i = 1; Fp4Cfg<BN>::split && i <= 3; ++i) {
                 attr[0].val.clusterDim.x = 1u << i;
-                cfg.gridDim = dim3((unsigned)(2 * d->num_sms >> i << i), 1, 1);
+                cfg.gridDim = dim3((unsigned)(d->num_sms >> i << i), 1, 1);
                 int nc = 0;
                 if (cudaOccupancyMaxActiveClusters(&nc, k, &cfg) != cudaSuccess) return FP8BS_ERR_CUDA;
-                d->fp4_clusters[slot][i].store(nc, std::memory_order_relaxed);
+                d->fp4_clusters[slot][i].store(nc <= d->num_sms >> i ? 2 * nc : nc, std::memory_order_relaxed);
             }
             d->fp4_attr_set[slot].store(true, std::memory_order_release);
         }

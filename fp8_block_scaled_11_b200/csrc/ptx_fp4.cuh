@@ -78,11 +78,13 @@ __device__ __forceinline__ uint32_t cluster_nctarank()
     return r;
 }
 
-// The two halves of cluster_sync_all: work between them runs while the peers
-// arrive.  Every thread of the CTA executes both.
+// The two halves of a cluster barrier: work between them runs while the peers
+// arrive.  Every thread of the CTA executes both.  The arrival orders no memory
+// (a releasing one cost 800 cycles here): what the peers may use are mbarriers,
+// published by fence_barrier_init.
 __device__ __forceinline__ void cluster_arrive()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait()
 {
