@@ -11,15 +11,13 @@
 
 namespace fp8bs {
 
-// The four scale bytes of a 128-column chunk from the byte of each of its four
-// groups, held by lanes 0, 4, 8, 12 of a half-warp; valid in its lane 0.
+// The four scale bytes of a 128-column chunk, from the byte of each group (the
+// same in the group's four lanes): the word in every lane of the half-warp.
 __device__ __forceinline__ uint32_t sf_gather_word(uint32_t byte, int lane)
 {
-    const int base = lane & 16;
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w |= __shfl_sync(0xffffffffu, byte, base + 4 * i) << (8 * i);
-    return w;
+    uint32_t w = byte << (8 * ((lane >> 2) & 3));
+    w |= __shfl_xor_sync(0xffffffffu, w, 4);
+    return w | __shfl_xor_sync(0xffffffffu, w, 8);
 }
 
 // Largest magnitude over the four lanes that share a group of 32 values.
@@ -138,29 +136,42 @@ __global__ void __launch_bounds__(256) fp4_quant_cols_kernel(const T* __restrict
 
 // --------------------------------------------------------------------------
 // Codes and scale tiles -> values (bf16 or fp32): exact, except that a value
-// outside the output type's range rounds as the type does.
+// outside the output type's range rounds as the type does.  The same partition as
+// fp4_quant_rows_kernel: a CTA owns a scale tile.
 // --------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(256) fp4_dequant_kernel(const uint8_t* __restrict__ q, int64_t ldq,
                                                           const uint8_t* __restrict__ sf, int64_t rows, int64_t cols,
                                                           int64_t kcs, T* __restrict__ out, int64_t ldo)
 {
-    const int64_t g = cols >> 5;                  // groups per row
-    const int64_t total = rows * g * 4;           // eight values each
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t r = i / (g * 4);
-        const int64_t v = i - r * (g * 4);        // eighth of the row
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(q + r * ldq + v * 4);
-        const uint32_t byte = sf[sf_word_offset(r, v >> 4, kcs) + ((v >> 2) & 3)];
-        float f[8];
-        mx4_unpack8(w, mx4_scale_value(byte), f);
-        T* dst = out + r * ldo + v * 8;
-        if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint4*>(dst) = make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]),
-                                                        cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7]));
-        } else {
-            *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<float4*>(dst + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    const int hw = threadIdx.x >> 4;
+    const int64_t rb = blockIdx.x / kcs, kc = blockIdx.x - rb * kcs;
+    const int64_t c = kc * 128 + (threadIdx.x & 15) * 8;
+    if (c >= cols) return;                       // cols % 32 == 0: a group is all in or all out
+    const int group = (threadIdx.x >> 2) & 3;
+    uint32_t w[8], byte[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = rb * 128 + hw + 16 * (i & 1) + 32 * (i >> 1);
+        if (r < rows) {
+            w[i] = __ldcs(reinterpret_cast<const uint32_t*>(q + r * ldq + (c >> 1)));
+            byte[i] = sf[sf_word_offset(r, kc, kcs) + group];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = rb * 128 + hw + 16 * (i & 1) + 32 * (i >> 1);
+        if (r < rows) {
+            float f[8];
+            mx4_unpack8(w[i], mx4_scale_value(byte[i]), f);
+            T* dst = out + r * ldo + c;
+            if constexpr (sizeof(T) == 2) {
+                __stcs(reinterpret_cast<uint4*>(dst), make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]),
+                                                                 cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7])));
+            } else {
+                __stcs(reinterpret_cast<float4*>(dst), make_float4(f[0], f[1], f[2], f[3]));
+                __stcs(reinterpret_cast<float4*>(dst + 4), make_float4(f[4], f[5], f[6], f[7]));
+            }
         }
     }
 }

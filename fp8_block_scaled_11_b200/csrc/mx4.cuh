@@ -16,6 +16,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda_fp16.h>
 #include "ptx.cuh"
 
 namespace fp8bs {
@@ -60,13 +61,20 @@ __device__ __forceinline__ uint32_t mx4_pack8(const float (&f)[8], float s)
 // Eight codes -> eight values times r (exact: a code's value has two bits).
 __device__ __forceinline__ void mx4_unpack8(uint32_t w, float r, float (&f)[8])
 {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t c = (w >> (4 * i)) & 15u;
-        // E2M1 -> fp32: exponent bias 1 -> 127; codes 0 and 1 (0 and 0.5) are the subnormals
-        const uint32_t m = c & 7u;
-        const float mag = m < 2u ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-        f[i] = __uint_as_float(__float_as_uint(mag * r) | (c >> 3) << 31);
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        f[2 * i] = v.x * r;
+        f[2 * i + 1] = v.y * r;
     }
 }
 

@@ -389,8 +389,9 @@ fp8bs_status fp4_dequant_1x32(const uint8_t* q, int64_t ldq, const uint8_t* scal
     DeviceInfo* d = nullptr;
     fp8bs_status st = get_device(&d);
     if (st != FP8BS_OK) return st;
-    const int64_t total = rows * (cols / 8);
-    const unsigned grid = (unsigned)std::min<int64_t>(cdiv(total, 256), (int64_t)d->num_sms * 64);
+    const int64_t tiles = cdiv(rows, 128) * cdiv(cols, 128);
+    if (tiles > INT32_MAX) return FP8BS_ERR_INVALID_ARG;
+    const unsigned grid = (unsigned)tiles;
     if (ot == FP8BS_BF16)
         fp4_dequant_kernel<<<grid, 256, 0, stream>>>(q, ldq, scale_tiles, rows, cols, cdiv(cols, 128),
                                                      static_cast<__nv_bfloat16*>(out), ldo);
