@@ -31,71 +31,170 @@ fp8bs_status check_norm(const NormParams& p, fp8bs_dtype xt, fp8bs_dtype wt)
     return FP8BS_OK;
 }
 
+// Threads per row (16, or a multiple of 32) and eights per thread for a row of
+// `eights` eights: the pair that leaves the fewest threads idle, at most max_tx
+// threads; among equals the first of `order`.
+struct RowShape {
+    int tx, vpt;                // vpt == 0: the row is too wide
+};
+
+RowShape row_shape(int64_t eights, int64_t max_tx, const int (&order)[3])
+{
+    RowShape best = {0, 0};
+    int64_t best_idle = INT64_MAX;
+    for (int vpt : order) {
+        int64_t tx = cdiv(eights, vpt);
+        tx = tx <= 16 ? 16 : round32(tx);
+        if (tx <= max_tx && tx * vpt - eights < best_idle) {
+            best_idle = tx * vpt - eights;
+            best = {(int)tx, vpt};
+        }
+    }
+    return best;
+}
+
 template <typename T, int BITS>
 fp8bs_status launch_norm(DeviceInfo* d, const NormParams& p, cudaStream_t stream)
 {
     const int64_t eights = cdiv(p.cols, 8);
-    // eights per thread: one where few rows leave the GPU idle otherwise (a row's
-    // latency is what counts), four where many rows keep it busy
-    const int vpt = p.rows <= 2 * d->num_sms && eights <= 1024 ? 1 : eights <= 4 * 512 ? 4 : 0;
-    if (vpt == 0) {
+    // one eight per thread where few rows would leave the GPU idle otherwise (a
+    // row's latency is what counts); else up to four, over which a row's and its
+    // groups' own work is spread
+    RowShape sh = {(int)round32(eights), 1};
+    if (p.rows > 2 * d->num_sms || eights > 1024) sh = row_shape(eights, 512, {4, 2, 1});
+    if (sh.vpt == 0) {
         rmsnorm_quant_wide_kernel<T, BITS><<<(unsigned)p.rows, 512, 0, stream>>>(p);
         return launch_status();
     }
-    const int64_t tx = round32(cdiv(eights, vpt));
-    const int64_t ty = std::max<int64_t>(1, std::min<int64_t>(256 / tx, p.rows));
-    const dim3 block((unsigned)tx, (unsigned)ty);
-    const unsigned grid = (unsigned)cdiv(p.rows, ty);
-    if (vpt == 1) rmsnorm_quant_kernel<T, BITS, 1><<<grid, block, 0, stream>>>(p);
+    const int ty = (int)std::max<int64_t>(1, std::min<int64_t>({256 / sh.tx, p.rows, sh.tx > 32 ? 8 : 16}));
+    const dim3 block((unsigned)sh.tx, (unsigned)(sh.tx == 16 ? (ty + 1) / 2 * 2 : ty));
+    const unsigned grid = (unsigned)cdiv(p.rows, block.y);
+    if (sh.vpt == 1) rmsnorm_quant_kernel<T, BITS, 1><<<grid, block, 0, stream>>>(p);
+    else if (sh.vpt == 2) rmsnorm_quant_kernel<T, BITS, 2><<<grid, block, 0, stream>>>(p);
     else rmsnorm_quant_kernel<T, BITS, 4><<<grid, block, 0, stream>>>(p);
     return launch_status();
 }
 
-// The backward's launch: threads per row, rows per CTA, CTAs, and the bytes of
-// its workspace.  Rows of up to 8192 columns are read once (kBackVpt eights a
-// thread); wider ones take two launches.
-constexpr int kBackVpt = 2;
-constexpr int64_t kBackParts = 1024;            // rows of partial sums at most
-
+// The backward's launch and the bytes of its workspace.  Rows are read once, over
+// a ring, where two slots of one fit (up to 16384 columns of bf16, 8192 of fp32);
+// wider ones take two launches.
 struct BackPlan {
-    bool wide;
-    int64_t tx, ty, grid, parts;
+    RowShape shape;             // vpt == 0: wide rows
+    int ty, slots, per_sm;      // rows per block of the ring, its depth, CTAs per SM
+    uint32_t smem;
+    int64_t grid, parts;
     size_t dot_off, bytes;
 };
 
-BackPlan plan_back(int64_t rows, int64_t cols, int num_sms)
+constexpr uint32_t kRingSmem = 222 * 1024;      // of an SM's shared memory
+
+BackPlan plan_back(int64_t rows, int64_t cols, int64_t elem, int mats, int num_sms)
 {
-    BackPlan b;
+    BackPlan b = {};
     const int64_t eights = cdiv(cols, 8);
-    b.wide = eights > kBackVpt * 512;
-    if (b.wide) {
-        b.tx = 256;
-        b.ty = 1;
-        b.grid = std::max<int64_t>(1, std::min<int64_t>(rows, 8 * num_sms / cdiv(cols, 2048)));
-        b.parts = b.grid;
-    } else {
-        b.tx = round32(cdiv(eights, kBackVpt));
-        b.ty = std::max<int64_t>(1, std::min<int64_t>(256 / b.tx, rows));
-        const int64_t per_sm = std::max<int64_t>(1, 1024 / (b.tx * b.ty));
-        b.grid = std::min<int64_t>({cdiv(rows, b.ty), per_sm * num_sms, kBackParts / b.ty});
-        b.parts = b.grid * b.ty;
+    const uint32_t row_bytes = (uint32_t)std::min<int64_t>(cols * elem, kRingSmem);
+    // four, two or one eights per thread: what keeps the most threads of an SM at
+    // work, 512 at most, over CTAs of 256 (or of one row's) that each have room
+    // for two slots; more eights a thread among equals
+    double best = 0.;
+    for (int vpt = 4; vpt >= 1; vpt /= 2) {
+        int64_t tx = cdiv(eights, vpt);
+        tx = tx <= 16 ? 16 : round32(tx);
+        if (tx > 512) continue;
+        int ty = std::max(1, (int)(256 / tx));
+        while (ty > 1 && cdiv(rows, ty) < num_sms) ty /= 2;             // few rows: over more SMs
+        if (tx == 16) ty = (ty + 1) / 2 * 2;                            // whole warps
+        const uint32_t slot = ring_smem(row_bytes, ty, mats, 1);
+        const int per_sm = (int)std::min<int64_t>(512 / (tx * ty), kRingSmem / (2 * slot + 1024));
+        const double busy = (double)per_sm * (double)ty * (double)eights / vpt;
+        if (per_sm < 1 || busy <= best) continue;
+        best = busy;
+        b.shape = {(int)tx, vpt};
+        b.ty = ty;
+        b.per_sm = per_sm;
+        b.slots = (int)std::min<uint32_t>(4, (kRingSmem / (uint32_t)per_sm - 1024) / slot);
+        b.smem = ring_smem(row_bytes, ty, mats, b.slots);
     }
+    if (b.shape.vpt > 0) b.grid = std::min<int64_t>(cdiv(rows, b.ty), (int64_t)b.per_sm * num_sms);
+    else b.grid = std::max<int64_t>(1, std::min<int64_t>(rows, 8 * num_sms / cdiv(cols, 2048)));
+    b.parts = b.grid;
     b.dot_off = (size_t)(b.parts * cols) * sizeof(float);
-    b.bytes = b.dot_off + (b.wide ? (size_t)((rows + 3) / 4 * 4) * sizeof(float) : 0);
+    b.bytes = b.dot_off + (b.shape.vpt == 0 ? (size_t)((rows + 3) / 4 * 4) * sizeof(float) : 0);
     return b;
 }
 
-template <typename T>
-fp8bs_status launch_norm_back(const BackPlan& b, const NormBackParams& p, float* dweight, cudaStream_t stream)
+template <typename T, int VPT, int THREADS, bool WREG>
+fp8bs_status launch_back_ring(DeviceInfo* d, const BackPlan& b, const NormBackParams& p, cudaStream_t stream)
 {
-    if (b.wide) {
-        rmsnorm_back_dot_kernel<T><<<(unsigned)p.rows, 512, 0, stream>>>(p);
-        const dim3 grid((unsigned)cdiv(p.cols, 2048), (unsigned)b.grid);
-        rmsnorm_back_wide_kernel<T><<<grid, 256, 0, stream>>>(p);
-    } else {
-        rmsnorm_back_kernel<T, kBackVpt><<<(unsigned)b.grid, dim3((unsigned)b.tx, (unsigned)b.ty), 0, stream>>>(p);
+    auto k = rmsnorm_back_kernel<T, VPT, THREADS, WREG>;
+    constexpr int slot = (sizeof(T) == 4 ? 1 : 0) + (WREG ? 2 : 0) + (VPT >> 1) * 4 + (THREADS > 256 ? 12 : 0);
+    if (!d->ring_attr_set[slot].load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        if (!d->ring_attr_set[slot].load(std::memory_order_relaxed)) {
+            if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingSmem) != cudaSuccess)
+                return FP8BS_ERR_CUDA;
+            d->ring_attr_set[slot].store(true, std::memory_order_release);
+        }
     }
-    rmsnorm_dw_kernel<<<(unsigned)cdiv(p.cols, 32), 256, 0, stream>>>(p.part, (int)b.parts, p.cols, dweight);
+    RowRing g = {};
+    g.src[0] = p.dy;
+    g.src[1] = p.h;
+    g.src[2] = p.dh;
+    g.pitch[0] = p.lddy * (int64_t)sizeof(T);
+    g.pitch[1] = p.ldh * (int64_t)sizeof(T);
+    g.pitch[2] = p.lddh * (int64_t)sizeof(T);
+    g.rows = p.rows;
+    g.row_bytes = (uint32_t)(p.cols * sizeof(T));
+    g.tx = b.shape.tx;
+    g.ty = b.ty;
+    g.slots = b.slots;
+    g.err = d->err_ptr;
+    k<<<(unsigned)b.grid, g.tx * g.ty, b.smem, stream>>>(p, g);
+    return launch_status();
+}
+
+template <typename T, bool WREG>
+fp8bs_status launch_back_rows(DeviceInfo* d, const BackPlan& b, const NormBackParams& p, cudaStream_t stream)
+{
+    // one row's threads are over 256 only where the ring leaves room for one CTA
+    // (rows of bf16 with four eights a thread, of fp32 with four or two)
+    if (b.shape.tx * b.ty > 256) {
+        if constexpr (sizeof(T) == 4)
+            if (b.shape.vpt == 2) return launch_back_ring<T, 2, 512, WREG>(d, b, p, stream);
+        return launch_back_ring<T, 4, 512, WREG>(d, b, p, stream);
+    }
+    if (b.shape.vpt == 1) return launch_back_ring<T, 1, 256, WREG>(d, b, p, stream);
+    if (b.shape.vpt == 2) return launch_back_ring<T, 2, 256, WREG>(d, b, p, stream);
+    return launch_back_ring<T, 4, 256, WREG>(d, b, p, stream);
+}
+
+template <typename T>
+fp8bs_status launch_norm_back(DeviceInfo* d, const BackPlan& b, const NormBackParams& p, float* dweight,
+                              cudaStream_t stream)
+{
+    fp8bs_status st;
+    if (b.shape.vpt == 0) {
+        rmsnorm_back_dot_kernel<T><<<(unsigned)p.rows, 512, 0, stream>>>(p);
+        rmsnorm_back_wide_kernel<T><<<dim3((unsigned)cdiv(p.cols, 2048), (unsigned)b.grid), 256, 0, stream>>>(p);
+        st = launch_status();
+    } else {
+        st = (p.w_f32 != 0) == (sizeof(T) == 4) ? launch_back_rows<T, true>(d, b, p, stream)
+                                                : launch_back_rows<T, false>(d, b, p, stream);
+    }
+    if (st != FP8BS_OK) return st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)cdiv(p.cols, 32), 1, 1);
+    cfg.blockDim = dim3(512, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const float* part = p.part;
+    const int parts = (int)b.parts;
+    const int64_t cols = p.cols;
+    if (cudaLaunchKernelEx(&cfg, rmsnorm_dw_kernel, part, parts, cols, dweight) != cudaSuccess) return FP8BS_ERR_CUDA;
     return launch_status();
 }
 
@@ -274,7 +373,7 @@ fp8bs_status fp8_rmsnorm_quant_1x128(const void* x, int64_t ldx, const void* res
 {
     if (rule != FP8BS_SCALE_RULE_FP32 && rule != FP8BS_SCALE_RULE_POW2) return FP8BS_ERR_UNSUPPORTED;
     const NormParams p = {x, residual, weight, h, rstd, y, q, scale_inv, rows, cols, ldx, ld_res, ldh, ldy, ldq,
-                          ld_scale, eps, wt == FP8BS_F32, rule == FP8BS_SCALE_RULE_POW2};
+                          ld_scale, eps, 1.f / (float)cols, wt == FP8BS_F32, rule == FP8BS_SCALE_RULE_POW2};
     fp8bs_status st = check_norm(p, xt, wt);
     if (st != FP8BS_OK) return st;
     if (ldq < cols || ld_scale < rows) return FP8BS_ERR_INVALID_ARG;
@@ -290,7 +389,7 @@ fp8bs_status fp4_rmsnorm_quant_1x32(const void* x, int64_t ldx, const void* resi
                                     uint8_t* scale_tiles, cudaStream_t stream)
 {
     const NormParams p = {x, residual, weight, h, rstd, y, q, scale_tiles, rows, cols, ldx, ld_res, ldh, ldy, ldq,
-                          cdiv(cols, 128), eps, wt == FP8BS_F32, 0};
+                          cdiv(cols, 128), eps, 1.f / (float)cols, wt == FP8BS_F32, 0};
     fp8bs_status st = check_norm(p, xt, wt);
     if (st != FP8BS_OK) return st;
     if (cols % 32) return FP8BS_ERR_ALIGNMENT;
@@ -303,7 +402,12 @@ fp8bs_status fp4_rmsnorm_quant_1x32(const void* x, int64_t ldx, const void* resi
 size_t fp8bs_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols)
 {
     if (rows < 1 || cols < 1) return 0;
-    return plan_back(rows, cols, num_sms_current()).bytes;
+    // the largest need over the types and over a call with or without dh
+    const int sms = num_sms_current();
+    size_t n = 0;
+    for (int64_t elem = 2; elem <= 4; elem += 2)
+        for (int mats = 2; mats <= 3; ++mats) n = std::max(n, plan_back(rows, cols, elem, mats, sms).bytes);
+    return n;
 }
 
 fp8bs_status fp8bs_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* dh,
@@ -325,14 +429,15 @@ fp8bs_status fp8bs_rmsnorm_backward(const void* dy, int64_t lddy, const void* h,
     DeviceInfo* d = nullptr;
     fp8bs_status st = get_device(&d);
     if (st != FP8BS_OK) return st;
-    const BackPlan b = plan_back(rows, cols, d->num_sms);
-    if (workspace == nullptr || workspace_bytes < b.bytes) return FP8BS_ERR_WORKSPACE;
+    const BackPlan b = plan_back(rows, cols, e, dh != nullptr ? 3 : 2, d->num_sms);
+    if (workspace == nullptr || workspace_bytes < fp8bs_rmsnorm_backward_workspace_size(rows, cols))
+        return FP8BS_ERR_WORKSPACE;
     if (!aligned16(workspace)) return FP8BS_ERR_ALIGNMENT;
     const NormBackParams p = {dy, h, dh, weight, rstd, dx, static_cast<float*>(workspace),
                               reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + b.dot_off), rows, cols, lddy,
                               ldh, lddh, lddx, wt == FP8BS_F32};
-    return xt == FP8BS_BF16 ? launch_norm_back<__nv_bfloat16>(b, p, dweight, stream)
-                            : launch_norm_back<float>(b, p, dweight, stream);
+    return xt == FP8BS_BF16 ? launch_norm_back<__nv_bfloat16>(d, b, p, dweight, stream)
+                            : launch_norm_back<float>(d, b, p, dweight, stream);
 }
 
 size_t fp4_scale_tiles_size(int64_t rows, int64_t cols)

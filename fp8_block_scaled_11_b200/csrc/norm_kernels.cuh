@@ -18,6 +18,7 @@
 #include <cuda_bf16.h>
 #include "ptx.cuh"
 #include "mx4.cuh"
+#include "ptx_fp4.cuh"
 #include "quant_kernels.cuh"
 #include "fp4_quant_kernels.cuh"
 
@@ -34,91 +35,257 @@ struct NormParams {
     void* scale;                // fp32 grid (8 bits) or scale tiles (4 bits)
     int64_t rows, cols, ldx, ldr, ldh, ldy, ldq;
     int64_t lds;                // leading dimension of the fp32 grid, or scale tiles per row block
-    float eps;
+    float eps, inv_cols;        // inv_cols = 1 / cols
     int w_f32, pow2;
 };
 
-// Eight weights as fp32 (bf16 or fp32 in memory).
-__device__ __forceinline__ void load_weight8(const void* w, int w_f32, int64_t c, float (&f)[8])
+// Eight values as four fp32 pairs: the arithmetic below is packed (two lanes an
+// instruction), since these kernels in bf16 come close to the issue rate before
+// they reach the memory's.
+struct Eight {
+    float2 v[4];
+};
+
+template <typename T>
+__device__ __forceinline__ Eight eight_of(const Vec8<T>& a)
 {
-    if (w_f32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c);
-        const float4 a = __ldg(p), b = __ldg(p + 1);
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    Eight e;
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t w[4] = {a.raw.x, a.raw.y, a.raw.z, a.raw.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e.v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
     } else {
-        Vec8<__nv_bfloat16> v;
-        v.raw = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + c));
-        v.get(f);
+        e.v[0] = make_float2(a.a.x, a.a.y);
+        e.v[1] = make_float2(a.a.z, a.a.w);
+        e.v[2] = make_float2(a.b.x, a.b.y);
+        e.v[3] = make_float2(a.b.z, a.b.w);
+    }
+    return e;
+}
+
+__device__ __forceinline__ Eight eight_zero()
+{
+    Eight e;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e.v[i] = make_float2(0.f, 0.f);
+    return e;
+}
+
+// a + b, rounded to T.  bf16: the packed addition rounds the exact sum once; so
+// does rounding the fp32 sum (the sum of two 8-bit significands is exact in fp32,
+// or else next to one of them and far from a tie).
+template <typename T>
+__device__ __forceinline__ void add_round(Vec8<T>& a, const Vec8<T>& b)
+{
+    if constexpr (sizeof(T) == 2) {
+        uint32_t* x = reinterpret_cast<uint32_t*>(&a.raw);
+        const uint32_t* y = reinterpret_cast<const uint32_t*>(&b.raw);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(x[i]) : "r"(x[i]), "r"(y[i]));
+    } else {
+        a.a.x += b.a.x; a.a.y += b.a.y; a.a.z += b.a.z; a.a.w += b.a.w;
+        a.b.x += b.b.x; a.b.y += b.b.y; a.b.z += b.b.z; a.b.w += b.b.w;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, const Vec8<T>& a)
+{
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4*>(p) = a.raw;
+    } else {
+        *reinterpret_cast<float4*>(p) = a.a;
+        *reinterpret_cast<float4*>(p + 4) = a.b;
     }
 }
 
 // Eight fp32 values rounded to T, stored (16-byte stores).
-__device__ __forceinline__ void store8(float* p, const float (&f)[8])
+__device__ __forceinline__ void store8(float* p, const Eight& e)
 {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    *reinterpret_cast<float4*>(p) = make_float4(e.v[0].x, e.v[0].y, e.v[1].x, e.v[1].y);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(e.v[2].x, e.v[2].y, e.v[3].x, e.v[3].y);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8])
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const Eight& e)
 {
-    *reinterpret_cast<uint4*>(p) = make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]),
-                                              cvt_bf16x2(f[6], f[7]));
+    *reinterpret_cast<uint4*>(p) = make_uint4(cvt_bf16x2(e.v[0].x, e.v[0].y), cvt_bf16x2(e.v[1].x, e.v[1].y),
+                                              cvt_bf16x2(e.v[2].x, e.v[2].y), cvt_bf16x2(e.v[3].x, e.v[3].y));
 }
 
-// f rounded to T's precision, in place.
-template <typename T>
-__device__ __forceinline__ void round8(float (&f)[8])
+// Eight weights as fp32 (bf16 or fp32 in memory).
+__device__ __forceinline__ Eight load_weight8(const void* w, int w_f32, int64_t c)
 {
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t p = cvt_bf16x2(f[2 * i], f[2 * i + 1]);
-            f[2 * i] = __uint_as_float(p << 16);
-            f[2 * i + 1] = __uint_as_float(p & 0xFFFF0000u);
-        }
+    if (w_f32) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c);
+        Vec8<float> v;
+        v.a = __ldg(p);
+        v.b = __ldg(p + 1);
+        return eight_of(v);
     }
+    Vec8<__nv_bfloat16> v;
+    v.raw = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + c));
+    return eight_of(v);
 }
 
-// Sum over the blockDim.x threads of this row (blockDim.x a multiple of 32; all
-// threads of the CTA take part).  `part` holds one float per warp of the CTA.
-__device__ __forceinline__ float row_sum(float v, float* part)
+__device__ __forceinline__ float sum_squares(const Eight& e, float acc)
 {
+    float2 s = make_float2(acc, 0.f);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
-    float* mine = part + threadIdx.y * warps;
-    if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = v;
-    __syncthreads();
+    for (int i = 0; i < 4; ++i) s = ffma2(e.v[i], e.v[i], s);
+    return s.x + s.y;
+}
+
+// 1 / sqrt(a): the hardware's approximation and one Newton step (about one
+// rounding from the exact value).
+__device__ __forceinline__ float rstd_of(float sum, float inv_cols, float eps)
+{
+    const float a = fmaf(sum, inv_cols, eps);
+    const float r = rsqrtf(a);
+    return r * fmaf(-0.5f * a * r, r, 1.5f);
+}
+
+// y = h * rstd * w
+__device__ __forceinline__ Eight normalise(const Eight& h, float rstd, const Eight& w)
+{
+    const float2 k = make_float2(rstd, rstd);
+    Eight y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y.v[i] = fmul2(fmul2(h.v[i], k), w.v[i]);
+    return y;
+}
+
+// Sum of n (a multiple of 1, at most 32) warps' partial sums, 16 bytes a load.
+__device__ __forceinline__ float sum_parts(const float* part, int n)
+{
     float s = 0.f;
-    for (int i = 0; i < warps; ++i) s += mine[i];
+    for (int i = 0; i < n; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(part + i);
+        s += (v.x + (i + 1 < n ? v.y : 0.f)) + ((i + 2 < n ? v.z : 0.f) + (i + 3 < n ? v.w : 0.f));
+    }
     return s;
 }
 
-// Eight normalised values y of row r, columns c .. c+7 (zero past the last
-// column): quantised and stored with their group's scale.  Called by whole
-// warps, lane l holding the l-th eight columns of 256.
-template <int BITS>
-__device__ __forceinline__ void quantise_store(const NormParams& p, int64_t r, int64_t c, bool ok, const float (&y)[8])
+// Sum over the blockDim.x threads of this row (16, or a multiple of 32; all
+// threads of the CTA take part).
+__device__ __forceinline__ float row_sum(float v)
 {
-    const int lane = threadIdx.x & 31;
-    if constexpr (BITS == 8) {
-        float m = absmax8(y);
+    __shared__ __align__(16) float part[8][32];
 #pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float s = p.pow2 ? scale_rule<true>(m) : scale_rule<false>(m);
-        if (ok) {
-            *reinterpret_cast<uint2*>(p.q + r * p.ldq + c) = quant8(y, s);
-            if ((lane & 15) == 0) static_cast<float*>(p.scale)[r + (c >> 7) * p.lds] = __frcp_rn(s);
+    for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (blockDim.x == 16) return v;
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+    if (blockDim.x == 32) return v;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.y][threadIdx.x >> 5] = v;
+    __syncthreads();
+    return sum_parts(part[threadIdx.y], blockDim.x >> 5);
+}
+
+__device__ __forceinline__ float absmax(const Eight& e)
+{
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(fmaxf(m, fabsf(e.v[i].x)), fabsf(e.v[i].y));
+    return m;
+}
+
+// Largest of VPT values each over the lanes that differ in the bits TOP, TOP / 2,
+// .., 1: while more than one value is left, a step gives half of them away, so
+// that VPT = 4 takes 5 shuffles over 16 lanes instead of 16.  On return a lane
+// holds the maximum of value i whose bits are the lane's bits TOP (the higher
+// bit of i), TOP / 2.
+template <int VPT, int TOP>
+__device__ __forceinline__ float share_max(const float (&m)[VPT], int lane)
+{
+    float a;
+    int o = TOP;
+    if constexpr (VPT == 4) {
+        const bool hi = lane & TOP, lo = lane & (TOP >> 1);
+        float a0 = hi ? m[2] : m[0], a1 = hi ? m[3] : m[1];
+        a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[2], TOP));
+        a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, hi ? m[1] : m[3], TOP));
+        a = fmaxf(lo ? a1 : a0, __shfl_xor_sync(0xffffffffu, lo ? a0 : a1, TOP >> 1));
+        o = TOP >> 2;
+    } else if constexpr (VPT == 2) {
+        const bool hi = lane & TOP;
+        a = fmaxf(hi ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[1], TOP));
+        o = TOP >> 1;
+    } else {
+        a = m[0];
+    }
+#pragma unroll
+    for (; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return a;
+}
+
+// The value index a lane holds after share_max, and the lane (of its TOP * 2
+// lanes) that holds value i.
+template <int VPT, int TOP>
+__device__ __forceinline__ int share_index(int lane)
+{
+    if (VPT == 4) return ((lane & TOP) ? 2 : 0) + ((lane & (TOP >> 1)) ? 1 : 0);
+    return VPT == 2 && (lane & TOP) ? 1 : 0;
+}
+template <int VPT, int TOP>
+__device__ __forceinline__ int share_lane(int i)
+{
+    if (VPT == 4) return (i >> 1) * TOP + (i & 1) * (TOP >> 1);
+    return VPT == 2 ? i * TOP : 0;
+}
+
+// VPT eights of normalised values of row r, columns (i tx + x) 8 .. + 7 (zero past
+// the last column): quantised and stored with their groups' scales.  Whole warps
+// take part; 16 neighbouring lanes (4 for the groups of 32) hold a group.
+template <int BITS, int VPT>
+__device__ __forceinline__ void quantise_store(const NormParams& p, int64_t r, bool row_ok, int tx, int x,
+                                               const Eight (&y)[VPT])
+{
+    const int lane = threadIdx.x + threadIdx.y * blockDim.x & 31;
+    float m[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) m[i] = absmax(y[i]);
+    if constexpr (BITS == 8) {
+        const float top = share_max<VPT, 8>(m, lane);
+        const float mine = p.pow2 ? scale_rule<true>(top) : scale_rule<false>(top);
+        const int mi = share_index<VPT, 8>(lane);
+        const int mc = (mi * tx + (x & ~15)) * 8;               // first column of the lane's own group
+        const int own = VPT == 4 ? 3 : VPT == 2 ? 7 : 15;       // one of the lanes that hold the same group
+        if ((lane & own) == 0 && row_ok && mc < p.cols) static_cast<float*>(p.scale)[r + (mc >> 7) * p.lds] = __frcp_rn(mine);
+        uint8_t* q = p.q + r * p.ldq;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const float s = VPT == 1 ? mine : __shfl_sync(0xffffffffu, mine, (lane & 16) + share_lane<VPT, 8>(i));
+            const int c = (i * tx + x) * 8;
+            if (row_ok && c < p.cols) {
+                const float2 k = make_float2(s, s);
+                float2 t[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) t[j] = fmul2(y[i].v[j], k);
+                const uint32_t lo = cvt_e4m3x2(t[0].x, t[0].y) | (uint32_t)cvt_e4m3x2(t[1].x, t[1].y) << 16;
+                const uint32_t hi = cvt_e4m3x2(t[2].x, t[2].y) | (uint32_t)cvt_e4m3x2(t[3].x, t[3].y) << 16;
+                *reinterpret_cast<uint2*>(q + c) = make_uint2(lo, hi);
+            }
         }
     } else {
-        const uint32_t byte = mx4_scale_byte(group32_absmax(y));
-        const uint32_t codes = mx4_pack8(y, mx4_inv_scale(byte));
-        const uint32_t word = sf_gather_word(ok ? byte : 127u, lane);
-        if (ok) {
-            *reinterpret_cast<uint32_t*>(p.q + r * p.ldq + (c >> 1)) = codes;
-            if ((lane & 15) == 0)
-                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.scale) + sf_word_offset(r, c >> 7, p.lds)) = word;
+        const float top = share_max<VPT, 2>(m, lane);
+        const uint32_t mine = mx4_scale_byte(top);
+        const int mi = share_index<VPT, 2>(lane);
+        // the chunk's word: its four groups' bytes, groups past the last column 127
+        const int mc = (mi * tx + (x & ~3)) * 8;
+        const uint32_t word = sf_gather_word(mc < p.cols ? mine : 127u, lane);
+        const int own = VPT == 4 ? 12 : VPT == 2 ? 13 : 15;
+        const int chunk = (mi * tx + (x & ~15)) * 8;
+        if ((lane & own) == 0 && row_ok && chunk < p.cols)
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.scale) + sf_word_offset(r, chunk >> 7, p.lds)) = word;
+        uint8_t* q = p.q + r * p.ldq;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const uint32_t byte = VPT == 1 ? mine : __shfl_sync(0xffffffffu, mine, (lane & 28) + share_lane<VPT, 2>(i));
+            const int c = (i * tx + x) * 8;
+            if (row_ok && c < p.cols) {
+                const float f[8] = {y[i].v[0].x, y[i].v[0].y, y[i].v[1].x, y[i].v[1].y,
+                                    y[i].v[2].x, y[i].v[2].y, y[i].v[3].x, y[i].v[3].y};
+                *reinterpret_cast<uint32_t*>(q + (c >> 1)) = mx4_pack8(f, mx4_inv_scale(byte));
+            }
         }
     }
 }
@@ -133,61 +300,186 @@ __device__ __forceinline__ void quantise_store(const NormParams& p, int64_t r, i
 template <typename T, int BITS, int VPT>
 __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_quant_kernel(const NormParams p)
 {
-    __shared__ float part[32];
+    const int tx = blockDim.x, x = threadIdx.x;
     const int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool row_ok = r < p.rows;
-    const T* x = static_cast<const T*>(p.x) + r * p.ldx;
+    const T* src = static_cast<const T*>(p.x) + r * p.ldx;
     const T* res = static_cast<const T*>(p.res) + r * p.ldr;
-    float v[VPT][8];
-    {
-        Vec8<T> a[VPT], b[VPT];
+    Vec8<T> a[VPT], b[VPT];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int64_t c = ((int64_t)i * blockDim.x + threadIdx.x) * 8;
-            const bool ok = row_ok && c < p.cols;
-            a[i].zero();
-            b[i].zero();
-            if (ok) a[i].load(x + c);
-            if (ok && p.res != nullptr) b[i].load(res + c);
-        }
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int64_t c = ((int64_t)i * blockDim.x + threadIdx.x) * 8;
-            a[i].get(v[i]);
-            if (p.res != nullptr) {
-                float f[8];
-                b[i].get(f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] += f[j];
-                round8<T>(v[i]);
-                if (row_ok && c < p.cols) store8(static_cast<T*>(p.h) + r * p.ldh + c, v[i]);
-            }
-        }
+    for (int i = 0; i < VPT; ++i) {
+        const int c = (i * tx + x) * 8;
+        const bool ok = row_ok && c < p.cols;
+        a[i].zero();
+        b[i].zero();
+        if (ok) a[i].load(src + c);
+        if (ok && p.res != nullptr) b[i].load(res + c);
     }
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
-    ss = row_sum(ss, part);
-    const float rstd = __frcp_rn(__fsqrt_rn(ss / (float)p.cols + p.eps));
-    if (row_ok && threadIdx.x == 0 && p.rstd != nullptr) p.rstd[r] = rstd;
+    for (int i = 0; i < VPT; ++i) {
+        const int c = (i * tx + x) * 8;
+        if (p.res != nullptr) {
+            add_round(a[i], b[i]);
+            if (row_ok && c < p.cols) store_vec(static_cast<T*>(p.h) + r * p.ldh + c, a[i]);
+        }
+        ss = sum_squares(eight_of(a[i]), ss);
+    }
+    ss = row_sum(ss);
+    const float rstd = rstd_of(ss, p.inv_cols, p.eps);
+    if (row_ok && x == 0 && p.rstd != nullptr) p.rstd[r] = rstd;
+    Eight y[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int64_t c = ((int64_t)i * blockDim.x + threadIdx.x) * 8;
-        const bool ok = row_ok && c < p.cols;
-        float y[8];
-        if (ok) {
-            load_weight8(p.w, p.w_f32, c, y);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] *= v[i][j] * rstd;
-            if (p.y != nullptr) store8(static_cast<T*>(p.y) + r * p.ldy + c, y);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = 0.f;
+        const int c = (i * tx + x) * 8;
+        y[i] = eight_zero();
+        if (row_ok && c < p.cols) {
+            y[i] = normalise(eight_of(a[i]), rstd, load_weight8(p.w, p.w_f32, c));
+            if (p.y != nullptr) store8(static_cast<T*>(p.y) + r * p.ldy + c, y[i]);
         }
-        quantise_store<BITS>(p, r, c, ok, y);
     }
+    quantise_store<BITS, VPT>(p, r, row_ok, tx, x, y);
+}
+
+// --------------------------------------------------------------------------
+// A ring of row blocks in shared memory: a CTA goes over blocks blockIdx.x,
+// + gridDim.x, .. of `ty` rows each, with `slots` blocks of up to three matrices
+// in flight (bulk copies, whole rows), so that the next rows arrive while this one
+// waits for its sum.  Warp 0 refills a slot once every warp has arrived on its
+// empty barrier.  The backward pass uses it, whose CTAs must live long to keep
+// their sums of dw; the forward pass is faster with a CTA per row and many of them
+// on an SM (16640 x 8192 bf16 with residual: 153 us, over a ring 203).
+//
+// A wait that runs out (bounded as everywhere) raises the error flag and the
+// CTA's abort flag and goes on: the row's barriers stay matched and the kernel
+// ends, since every later wait returns at once.
+// --------------------------------------------------------------------------
+constexpr int kRingMats = 3;
+constexpr uint64_t kRingWaitNs = 2000000000ull;
+
+struct RowRing {
+    const void* src[kRingMats];     // nullptr: none
+    int64_t pitch[kRingMats];       // bytes from row to row
+    int64_t rows;
+    uint32_t row_bytes;
+    int tx, ty, slots;              // threads per row, rows per block, ring depth
+    int* err;
+};
+
+struct RingView {
+    uint32_t base, bars;
+    uint32_t mat_bytes, slot_bytes;
+    int slots;
+    volatile int* abort_flag;
+    __device__ __forceinline__ uint32_t full(int s) const { return bars + 8u * s; }
+    __device__ __forceinline__ uint32_t empty(int s) const { return bars + 8u * (slots + s); }
+};
+
+// Shared memory of a ring: the slots, then its barriers and the abort flag.
+__host__ __device__ constexpr uint32_t ring_smem(uint32_t row_bytes, int ty, int mats, int slots)
+{
+    return (uint32_t)slots * (uint32_t)mats * (uint32_t)ty * row_bytes + 16u * (uint32_t)slots + 16u;
+}
+
+// Block b into slot s (warp 0).
+__device__ __forceinline__ void ring_issue(const RowRing& g, const RingView& v, int64_t b, int s)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t r0 = b * g.ty;
+    const int n = (int)min((int64_t)g.ty, g.rows - r0);
+    const uint32_t mats = v.slot_bytes / v.mat_bytes;
+    if (lane == 0) mbar_arrive_expect_tx(v.full(s), mats * (uint32_t)n * g.row_bytes);
+    __syncwarp();
+    uint32_t dst = v.base + (uint32_t)s * v.slot_bytes;
+#pragma unroll
+    for (int m = 0; m < kRingMats; ++m) {
+        if (g.src[m] == nullptr) continue;
+        const uint8_t* src = static_cast<const uint8_t*>(g.src[m]) + r0 * g.pitch[m];
+        if (g.pitch[m] == (int64_t)g.row_bytes) {
+            if (lane == 0) bulk_load(dst, src, (uint32_t)n * g.row_bytes, v.full(s));
+        } else {
+            for (int i = lane; i < n; i += 32)
+                bulk_load(dst + (uint32_t)i * g.row_bytes, src + i * g.pitch[m], g.row_bytes, v.full(s));
+        }
+        dst += v.mat_bytes;
+    }
+}
+
+// Barriers, and the CTA's first blocks.
+__device__ __forceinline__ RingView ring_init(const RowRing& g, uint8_t* smem, int64_t blocks)
+{
+    const int mats = (g.src[0] != nullptr) + (g.src[1] != nullptr) + (g.src[2] != nullptr);
+    RingView v;
+    v.base = smem_u32(smem);
+    v.mat_bytes = (uint32_t)g.ty * g.row_bytes;
+    v.slot_bytes = (uint32_t)mats * v.mat_bytes;
+    v.slots = g.slots;
+    v.bars = v.base + (uint32_t)g.slots * v.slot_bytes;
+    v.abort_flag = reinterpret_cast<volatile int*>(smem + (uint32_t)g.slots * v.slot_bytes + 16u * g.slots);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < g.slots; ++s) {
+            mbar_init(v.full(s), 1);
+            mbar_init(v.empty(s), blockDim.x >> 5);
+        }
+        *v.abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    if (threadIdx.x < 32)
+        for (int s = 0; s < g.slots; ++s)
+            if (blockIdx.x + (int64_t)s * gridDim.x < blocks) ring_issue(g, v, blockIdx.x + (int64_t)s * gridDim.x, s);
+    return v;
+}
+
+__device__ __forceinline__ bool ring_wait(const RowRing& g, const RingView& v, uint32_t bar, uint32_t parity)
+{
+    if (mbar_wait_limit(bar, parity, v.abort_flag, kRingWaitNs)) return true;
+    *v.abort_flag = 1;
+    atomicOr(g.err, 1);
+    return false;
+}
+
+// Slot s (in the `phase`-th use) of block b is read: warp 0 refills it.
+__device__ __forceinline__ void ring_release(const RowRing& g, const RingView& v, int64_t b, int64_t blocks, int s,
+                                             uint32_t phase)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(v.empty(s));
+    const int64_t next = b + (int64_t)g.slots * gridDim.x;
+    if (threadIdx.x < 32 && next < blocks) {
+        const bool ok = ring_wait(g, v, v.empty(s), phase);
+        if (__all_sync(0xffffffffu, ok)) ring_issue(g, v, next, s);
+    }
+}
+
+// Sum over the tx threads of row y of a block (tx = 16, or a multiple of 32; the
+// row's warps meet at named barrier 1 + y).  `part`: 16 floats, a multiple of
+// four for each row.
+__device__ __forceinline__ float ring_row_sum(float v, int tx, int x, int y, float* part)
+{
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (tx == 16) return v;
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+    if (tx == 32) return v;
+    float* mine = part + y * ((tx + 127) >> 7 << 2);
+    if ((x & 31) == 0) mine[x >> 5] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + y), "r"(tx) : "memory");
+    return sum_parts(mine, tx >> 5);
+}
+
+// Eight values of the ring's row at byte offset `at`.
+template <typename T>
+__device__ __forceinline__ Vec8<T> ring_vec(uint32_t at)
+{
+    Vec8<T> v;
+    if constexpr (sizeof(T) == 2) {
+        v.raw = lds_u4(at);
+    } else {
+        v.a = lds128(at);
+        v.b = lds128(at + 16);
+    }
+    return v;
 }
 
 // --------------------------------------------------------------------------
@@ -197,7 +489,6 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_quant_kernel(co
 template <typename T, int BITS>
 __global__ void __launch_bounds__(512) rmsnorm_quant_wide_kernel(const NormParams p)
 {
-    __shared__ float part[32];
     const int64_t r = blockIdx.x;
     const T* x = static_cast<const T*>(p.x) + r * p.ldx;
     const T* res = static_cast<const T*>(p.res) + r * p.ldr;
@@ -205,43 +496,31 @@ __global__ void __launch_bounds__(512) rmsnorm_quant_wide_kernel(const NormParam
     float ss = 0.f;
     for (int64_t c = (int64_t)threadIdx.x * 8; c < p.cols; c += (int64_t)blockDim.x * 8) {
         Vec8<T> a;
-        float v[8];
         a.load(x + c);
-        a.get(v);
         if (p.res != nullptr) {
-            float f[8];
-            a.load(res + c);
-            a.get(f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += f[j];
-            round8<T>(v);
-            store8(h + c, v);
+            Vec8<T> b;
+            b.load(res + c);
+            add_round(a, b);
+            store_vec(h + c, a);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss += v[j] * v[j];
+        ss = sum_squares(eight_of(a), ss);
     }
-    ss = row_sum(ss, part);
-    const float rstd = __frcp_rn(__fsqrt_rn(ss / (float)p.cols + p.eps));
+    ss = row_sum(ss);
+    const float rstd = rstd_of(ss, p.inv_cols, p.eps);
     if (threadIdx.x == 0 && p.rstd != nullptr) p.rstd[r] = rstd;
-    // each thread reads back what it wrote itself
+    // each thread reads back what it wrote itself; whole warps take part in the
+    // groups' maxima
     const T* src = p.res != nullptr ? h : x;
-    const int64_t top = (p.cols + 255) / 256 * 256;       // whole warps take part in the groups' maxima
+    const int64_t top = (p.cols + 255) / 256 * 256;
     for (int64_t c = (int64_t)threadIdx.x * 8; c < top; c += (int64_t)blockDim.x * 8) {
-        const bool ok = c < p.cols;
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = 0.f;
-        if (ok) {
+        Eight y[1] = {eight_zero()};
+        if (c < p.cols) {
             Vec8<T> a;
-            float v[8];
             a.load(src + c);
-            a.get(v);
-            load_weight8(p.w, p.w_f32, c, y);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] *= v[j] * rstd;
-            if (p.y != nullptr) store8(static_cast<T*>(p.y) + r * p.ldy + c, y);
+            y[0] = normalise(eight_of(a), rstd, load_weight8(p.w, p.w_f32, c));
+            if (p.y != nullptr) store8(static_cast<T*>(p.y) + r * p.ldy + c, y[0]);
         }
-        quantise_store<BITS>(p, r, c, ok, y);
+        quantise_store<BITS, 1>(p, r, true, 0, (int)(c >> 3), y);
     }
 }
 
@@ -261,76 +540,110 @@ struct NormBackParams {
     int w_f32;
 };
 
-// Rows of at most 8 * VPT * blockDim.x columns: a CTA goes over rows blockIdx.x
-// * blockDim.y + threadIdx.y, + gridDim.x * blockDim.y, ...; a thread keeps its
-// columns' weights and sums of dw in registers over all of them and leaves the
-// sums in row blockIdx.x * blockDim.y + threadIdx.y of `part`.
-template <typename T, int VPT>
-__global__ void __launch_bounds__(512) rmsnorm_back_kernel(const NormBackParams p)
+// Over a ring of dy, h and dh, rows of at most 8 * VPT * tx columns: a thread
+// keeps its columns' sums of dw in registers over all its rows, and its weights
+// where they have the rows' type (else they come from L1 with each row, beside
+// which the ring leaves little of L1: 16640 x 8192 bf16 took 200 to 245 us so);
+// the CTA's rows of sums are added at the end, in order, into row blockIdx.x of
+// `part`.  Two CTAs of 256 threads an SM hide each other's sums and barriers: one
+// of 512, over two rows at a time, took 247 us where two took 195.
+template <typename T, int VPT, int THREADS, bool WREG>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) rmsnorm_back_kernel(const NormBackParams p, const RowRing g)
 {
-    __shared__ float part[2][16];
-    float w[VPT][8], dw[VPT][8];
+    extern __shared__ __align__(128) uint8_t ring_raw[];
+    __shared__ __align__(16) float part[2][16];
+    const int64_t blocks = (g.rows + g.ty - 1) / g.ty;
+    const RingView v = ring_init(g, ring_raw, blocks);
+    // the reduction that follows may be set up from here on
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int y = (int)threadIdx.x / g.tx, x = (int)threadIdx.x - y * g.tx;
+    Eight dw[VPT];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int64_t c = ((int64_t)i * blockDim.x + threadIdx.x) * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[i][j] = dw[i][j] = 0.f;
-        if (c < p.cols) load_weight8(p.w, p.w_f32, c, w[i]);
-    }
-    const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    const float inv = 1.f / (float)p.cols;
-    int flip = 0;
-    for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < p.rows; base += step, flip ^= 1) {
-        const int64_t r = base + threadIdx.y;
-        const bool row_ok = r < p.rows;
-        const float rstd = row_ok ? p.rstd[r] : 0.f;
-        Vec8<T> a[VPT], b[VPT], d[VPT];
+    for (int i = 0; i < VPT; ++i) dw[i] = eight_zero();
+    Vec8<T> wr[WREG ? VPT : 1];
+    if constexpr (WREG) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int64_t c = ((int64_t)i * blockDim.x + threadIdx.x) * 8;
-            const bool ok = row_ok && c < p.cols;
-            a[i].zero();
-            b[i].zero();
-            d[i].zero();
-            if (ok) a[i].load(static_cast<const T*>(p.dy) + r * p.lddy + c);
-            if (ok) b[i].load(static_cast<const T*>(p.h) + r * p.ldh + c);
-            if (ok && p.dh != nullptr) d[i].load(static_cast<const T*>(p.dh) + r * p.lddh + c);
+            const int c = (i * g.tx + x) * 8;
+            wr[i].zero();
+            if (c < p.cols) wr[i].load(static_cast<const T*>(p.w) + c);
         }
-        float dot = 0.f;
+    }
+    auto weight = [&](int i, int c) {
+        if constexpr (WREG) return eight_of(wr[i]);
+        else return load_weight8(p.w, p.w_f32, c);
+    };
+    const float inv = 1.f / (float)p.cols;
+    int s = 0, flip = 0;
+    uint32_t phase = 0;
+    // a row's rstd is loaded a block ahead
+    const int64_t r_first = (int64_t)blockIdx.x * g.ty + y;
+    float rstd_next = r_first < p.rows ? __ldg(p.rstd + r_first) : 0.f;
+    for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x, flip ^= 1) {
+        const int64_t r = b * g.ty + y;
+        const bool row_ok = r < p.rows;
+        const float rstd = rstd_next;
+        const int64_t r_next = r + (int64_t)gridDim.x * g.ty;
+        rstd_next = r_next < p.rows ? __ldg(p.rstd + r_next) : 0.f;
+        ring_wait(g, v, v.full(s), phase);
+        const uint32_t at = v.base + (uint32_t)s * v.slot_bytes + (uint32_t)y * g.row_bytes;
+        // n = h rstd:  dw += dy n,  dot = sum dy w h
+        float2 dot2 = make_float2(0.f, 0.f);
+        const float2 rstd2 = make_float2(rstd, rstd);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            float dy[8], n[8];
-            a[i].get(dy);
-            b[i].get(n);
+            const int c = (i * g.tx + x) * 8;
+            if (row_ok && c < p.cols) {
+                const Eight w = weight(i, c);
+                const Eight dy = eight_of(ring_vec<T>(at + (uint32_t)c * sizeof(T)));
+                const Eight h = eight_of(ring_vec<T>(at + v.mat_bytes + (uint32_t)c * sizeof(T)));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                n[j] *= rstd;
-                const float t = dy[j] * n[j];
-                dw[i][j] += t;
-                dot += t * w[i][j];
+                for (int j = 0; j < 4; ++j) {
+                    const float2 t = fmul2(dy.v[j], h.v[j]);
+                    dw[i].v[j] = ffma2(t, rstd2, dw[i].v[j]);
+                    dot2 = ffma2(t, w.v[j], dot2);
+                }
             }
         }
-        // two sets of partial sums: a warp may be a row ahead of the slowest one
-        dot = row_sum(dot, part[flip]) * inv;
+        // two sets of partial sums: a row's warps may be a block apart
+        const float dot = ring_row_sum(dot2.x + dot2.y, g.tx, x, y, part[flip]);
+        // dx = rstd (dy w - n mean(g n)) + dh,  mean(g n) = rstd dot / cols
+        const float k = -(rstd * rstd) * rstd * (dot * inv);
+        const float2 k2 = make_float2(k, k);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int64_t c = ((int64_t)i * blockDim.x + threadIdx.x) * 8;
+            const int c = (i * g.tx + x) * 8;
             if (row_ok && c < p.cols) {
-                float dy[8], n[8], f[8];
-                a[i].get(dy);
-                b[i].get(n);
-                d[i].get(f);
+                const Eight w = weight(i, c);
+                const Eight dy = eight_of(ring_vec<T>(at + (uint32_t)c * sizeof(T)));
+                const Eight h = eight_of(ring_vec<T>(at + v.mat_bytes + (uint32_t)c * sizeof(T)));
+                Eight f = eight_zero();
+                if (p.dh != nullptr) f = eight_of(ring_vec<T>(at + 2 * v.mat_bytes + (uint32_t)c * sizeof(T)));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] += rstd * (dy[j] * w[i][j] - n[j] * rstd * dot);
+                for (int j = 0; j < 4; ++j)
+                    f.v[j] = ffma2(fmul2(dy.v[j], w.v[j]), rstd2, ffma2(h.v[j], k2, f.v[j]));
                 store8(static_cast<T*>(p.dx) + r * p.lddx + c, f);
             }
         }
+        ring_release(g, v, b, blocks, s, phase);
+        if (++s == g.slots) { s = 0; phase ^= 1u; }
     }
-    float* dst = p.part + ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * p.cols;
+    // the ring is empty: its memory takes the rows of sums
+    float* out = p.part + (int64_t)blockIdx.x * p.cols;
+    float* sums = reinterpret_cast<float*>(ring_raw);
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int64_t c = ((int64_t)i * blockDim.x + threadIdx.x) * 8;
-        if (c < p.cols) store8(dst + c, dw[i]);
+        const int c = (i * g.tx + x) * 8;
+        if (c < p.cols) store8(g.ty == 1 ? out + c : sums + (int64_t)y * p.cols + c, dw[i]);
+    }
+    if (g.ty > 1) {
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
+            float t = sums[c];
+            for (int i = 1; i < g.ty; ++i) t += sums[(int64_t)i * p.cols + c];
+            out[c] = t;
+        }
     }
 }
 
@@ -338,21 +651,18 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(const NormBackParams 
 template <typename T>
 __global__ void __launch_bounds__(512) rmsnorm_back_dot_kernel(const NormBackParams p)
 {
-    __shared__ float part[16];
     const int64_t r = blockIdx.x;
-    float dot = 0.f;
+    float2 dot2 = make_float2(0.f, 0.f);
     for (int64_t c = (int64_t)threadIdx.x * 8; c < p.cols; c += (int64_t)blockDim.x * 8) {
         Vec8<T> a, b;
-        float dy[8], h[8], w[8];
         a.load(static_cast<const T*>(p.dy) + r * p.lddy + c);
         b.load(static_cast<const T*>(p.h) + r * p.ldh + c);
-        a.get(dy);
-        b.get(h);
-        load_weight8(p.w, p.w_f32, c, w);
+        const Eight dy = eight_of(a), h = eight_of(b), w = load_weight8(p.w, p.w_f32, c);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dot += dy[j] * w[j] * h[j];
+        for (int j = 0; j < 4; ++j) dot2 = ffma2(fmul2(dy.v[j], h.v[j]), w.v[j], dot2);
     }
-    dot = row_sum(dot, part) * p.rstd[r];
+    float dot = dot2.x + dot2.y;
+    dot = row_sum(dot) * p.rstd[r];
     if (threadIdx.x == 0) p.dot[r] = dot / (float)p.cols;
 }
 
@@ -363,49 +673,54 @@ __global__ void __launch_bounds__(256) rmsnorm_back_wide_kernel(const NormBackPa
 {
     const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
     if (c >= p.cols) return;
-    float w[8], dw[8];
-    load_weight8(p.w, p.w_f32, c, w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[j] = 0.f;
+    const Eight w = load_weight8(p.w, p.w_f32, c);
+    Eight dw = eight_zero();
     for (int64_t r = blockIdx.y; r < p.rows; r += gridDim.y) {
-        const float rstd = p.rstd[r], dot = p.dot[r];
+        const float rstd = p.rstd[r], k = -(rstd * rstd) * p.dot[r];
+        const float2 rstd2 = make_float2(rstd, rstd), k2 = make_float2(k, k);
         Vec8<T> a, b, d;
         a.load(static_cast<const T*>(p.dy) + r * p.lddy + c);
         b.load(static_cast<const T*>(p.h) + r * p.ldh + c);
         d.zero();
         if (p.dh != nullptr) d.load(static_cast<const T*>(p.dh) + r * p.lddh + c);
-        float dy[8], n[8], f[8];
-        a.get(dy);
-        b.get(n);
-        d.get(f);
+        const Eight dy = eight_of(a), h = eight_of(b);
+        Eight f = eight_of(d);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            n[j] *= rstd;
-            dw[j] += dy[j] * n[j];
-            f[j] += rstd * (dy[j] * w[j] - n[j] * dot);
+        for (int j = 0; j < 4; ++j) {
+            dw.v[j] = ffma2(fmul2(dy.v[j], h.v[j]), rstd2, dw.v[j]);
+            f.v[j] = ffma2(fmul2(dy.v[j], w.v[j]), rstd2, ffma2(h.v[j], k2, f.v[j]));
         }
         store8(static_cast<T*>(p.dx) + r * p.lddx + c, f);
     }
     store8(p.part + (int64_t)blockIdx.y * p.cols + c, dw);
 }
 
-// dw[c] = sum over the parts, 32 columns a CTA: warp w adds parts w, w + 8, ...,
-// the warps' sums are added in order.
-__global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float* __restrict__ part, int parts, int64_t cols,
+// dw[c] = sum over the parts, 32 columns a CTA: warp w adds parts w, w + 16, ..,
+// eight loads in flight, and the warps' sums are added in order.  A programmatic
+// dependent of the pass that leaves the parts.
+__global__ void __launch_bounds__(512) rmsnorm_dw_kernel(const float* __restrict__ part, int parts, int64_t cols,
                                                          float* __restrict__ dw)
 {
-    __shared__ float s[8][32];
+    __shared__ float s[16][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float sum = 0.f;
-    if (c < cols)
-        for (int i = warp; i < parts; i += 8) sum += part[i * cols + c];
+    if (c < cols) {
+        for (int i = warp; i < parts; i += 128) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = i + 16 * j < parts ? __ldcg(part + (int64_t)(i + 16 * j) * cols + c) : 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum += v[j];
+        }
+    }
     s[warp][lane] = sum;
     __syncthreads();
     if (warp == 0 && c < cols) {
         float t = s[0][lane];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) t += s[i][lane];
+        for (int i = 1; i < 16; ++i) t += s[i][lane];
         dw[c] = t;
     }
 }
