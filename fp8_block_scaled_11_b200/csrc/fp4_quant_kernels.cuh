@@ -78,21 +78,25 @@ __global__ void __launch_bounds__(256) fp4_quant_rows_kernel(const T* __restrict
 
 // --------------------------------------------------------------------------
 // Groups along the rows; the transposed codes and their scale tiles are written
-// (row c of the output is column c of x).  A CTA owns 128 rows x 128 columns of
-// x, as 8 x 8 blocks: warp (wr, wc) covers 32 rows, i.e. one group, of 64
-// columns.
+// (row c of the output is column c of x).  A CTA owns 256 rows x 64 columns of x
+// (128 bytes of bf16 a row to read, 128 bytes a row of codes to write), as 8 x 8
+// blocks: warp w covers rows 32 w .. + 31, i.e. one group of each column.  The
+// codes pass through shared memory to leave in whole 16-byte pieces; its pieces
+// are permuted by the column's strip, so that a warp's words fall into 32 banks.
 // --------------------------------------------------------------------------
+constexpr int kQ4Rows = 256, kQ4Cols = 64;
+
 template <typename T>
-__global__ void __launch_bounds__(256) fp4_quant_cols_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) fp4_quant_cols_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
                                                              int64_t ldx, uint8_t* __restrict__ q, int64_t ldq,
                                                              uint8_t* __restrict__ sf, int64_t kcs, int64_t tiles_c)
 {
-    __shared__ __align__(16) uint8_t s_sf[kSfTileBytes];
+    __shared__ __align__(16) uint8_t s_q[kQ4Cols * 128];
+    __shared__ __align__(16) uint8_t s_sf[kQ4Cols * 8];
     const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
-    int strip, group, wr, wc;
-    qblock_coords(strip, group, wr, wc);
-    const int64_t r0 = tr * 128 + group * 8;
-    const int64_t c0 = tc * 128 + strip * 8;
+    const int w = threadIdx.x >> 5, strip = threadIdx.x & 7, part = (threadIdx.x >> 3) & 3;
+    const int64_t r0 = tr * kQ4Rows + w * 32 + part * 8;
+    const int64_t c0 = tc * kQ4Cols + strip * 8;
     const bool ok = r0 < rows && c0 < cols;     // rows % 32 == 0, cols % 16 == 0
     Block8x8<T> b;
 #pragma unroll
@@ -110,7 +114,6 @@ __global__ void __launch_bounds__(256) fp4_quant_cols_kernel(const T* __restrict
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const uint32_t byte = mx4_scale_byte(m[j]);
-        const float s = mx4_inv_scale(byte);
         float f[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -118,19 +121,26 @@ __global__ void __launch_bounds__(256) fp4_quant_cols_kernel(const T* __restrict
             b.row[i].get(g);
             f[i] = g[j];
         }
-        const uint32_t codes = mx4_pack8(f, s);
-        if (ok) *reinterpret_cast<uint32_t*>(q + (c0 + j) * ldq + (r0 >> 1)) = codes;
-        // the tile's byte of output row 8 strip + j, group wr (rows past x's last: a scale of one)
         const int row = strip * 8 + j;
-        if ((threadIdx.x & 31) < 8) s_sf[(row & 31) * 16 + (row >> 5) * 4 + wr] = (uint8_t)(r0 < rows ? byte : 127u);
+        *reinterpret_cast<uint32_t*>(s_q + row * 128 + ((w ^ strip) * 16) + part * 4) = mx4_pack8(f, mx4_inv_scale(byte));
+        // (rows past x's last: a scale of one)
+        if (part == 0) s_sf[row * 8 + w] = (uint8_t)(r0 < rows ? byte : 127u);
     }
     __syncthreads();
-    if (threadIdx.x < 128) {
-        const int64_t row = tc * 128 + threadIdx.x;
-        const int at = (threadIdx.x & 31) * 16 + (threadIdx.x >> 5) * 4;
-        if (row < cols)
-            *reinterpret_cast<uint32_t*>(sf + (tc * kcs + tr) * (int64_t)kSfTileBytes + at) =
-                *reinterpret_cast<const uint32_t*>(s_sf + at);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = (threadIdx.x >> 3) + 32 * i, piece = threadIdx.x & 7;
+        const int64_t c = tc * kQ4Cols + row, r = tr * kQ4Rows + piece * 32;
+        if (c < cols && r < rows)
+            *reinterpret_cast<uint4*>(q + c * ldq + (r >> 1)) =
+                *reinterpret_cast<const uint4*>(s_q + row * 128 + ((piece ^ (row >> 3)) * 16));
+    }
+    if (threadIdx.x < 2 * kQ4Cols) {
+        const int row = threadIdx.x >> 1, half = threadIdx.x & 1;
+        const int64_t c = tc * kQ4Cols + row, kc = tr * 2 + half;
+        if (c < cols && kc < kcs)
+            *reinterpret_cast<uint32_t*>(sf + sf_word_offset(c, kc, kcs)) =
+                *reinterpret_cast<const uint32_t*>(s_sf + row * 8 + half * 4);
     }
 }
 
@@ -149,12 +159,21 @@ __global__ void __launch_bounds__(256) fp4_dequant_kernel(const uint8_t* __restr
     const int64_t c = kc * 128 + (threadIdx.x & 15) * 8;
     if (c >= cols) return;                       // cols % 32 == 0: a group is all in or all out
     const int group = (threadIdx.x >> 2) & 3;
+    // bf16: a lane's eight codes make 16 bytes.  fp32: a pair of lanes takes its
+    // sixteen codes four at a time in turn, so that a pair stores 32 bytes in a row.
+    constexpr bool kWide = sizeof(T) == 4;
+    const int odd = threadIdx.x & 1;
     uint32_t w[8], byte[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t r = rb * 128 + hw + 16 * (i & 1) + 32 * (i >> 1);
         if (r < rows) {
-            w[i] = __ldcs(reinterpret_cast<const uint32_t*>(q + r * ldq + (c >> 1)));
+            if constexpr (kWide) {
+                const uint2 v = __ldcs(reinterpret_cast<const uint2*>(q + r * ldq + ((c - odd * 8) >> 1)));
+                w[i] = __byte_perm(v.x, v.y, odd ? 0x7632 : 0x5410);
+            } else {
+                w[i] = __ldcs(reinterpret_cast<const uint32_t*>(q + r * ldq + (c >> 1)));
+            }
             byte[i] = sf[sf_word_offset(r, kc, kcs) + group];
         }
     }
@@ -164,13 +183,14 @@ __global__ void __launch_bounds__(256) fp4_dequant_kernel(const uint8_t* __restr
         if (r < rows) {
             float f[8];
             mx4_unpack8(w[i], mx4_scale_value(byte[i]), f);
-            T* dst = out + r * ldo + c;
-            if constexpr (sizeof(T) == 2) {
-                __stcs(reinterpret_cast<uint4*>(dst), make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]),
-                                                                 cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7])));
-            } else {
+            if constexpr (kWide) {
+                T* dst = out + r * ldo + (c - odd * 4);
                 __stcs(reinterpret_cast<float4*>(dst), make_float4(f[0], f[1], f[2], f[3]));
-                __stcs(reinterpret_cast<float4*>(dst + 4), make_float4(f[4], f[5], f[6], f[7]));
+                __stcs(reinterpret_cast<float4*>(dst + 8), make_float4(f[4], f[5], f[6], f[7]));
+            } else {
+                __stcs(reinterpret_cast<uint4*>(out + r * ldo + c),
+                       make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]),
+                                  cvt_bf16x2(f[6], f[7])));
             }
         }
     }

@@ -63,6 +63,8 @@ def test_quant_rows(rows, cols, dtype):
     assert np.array_equal(got[ref.tile_index(rows, pad.shape[1])], pad)
     v = ops.fp4_dequant_1x32(q, s, out_dtype=torch.float32)
     assert np.array_equal(v.cpu().double().numpy(), ref.value(code, e))
+    v = ops.fp4_dequant_1x32(q, s)          # bf16 holds every value here but those past its range
+    assert np.array_equal(v.cpu().double().numpy(), torch.from_numpy(ref.value(code, e)).bfloat16().double().numpy())
     no_device_error()
 
 
