@@ -212,7 +212,18 @@ struct Fp4Plan {
 Fp4Plan plan_fp4(int64_t M, int64_t N, int64_t K, int num_sms)
 {
     Fp4Plan s;
-    s.pair = M > 128 && cdiv(N, kF4Pair) * cdiv(M, kF4Pair) >= num_sms / 2;
+    // CTA pairs, or single CTAs with 128 x 128 tiles once those are more than the
+    // SMs: by what each takes in us, waves of tiles (for single CTAs, which share an
+    // SM: tiles per SM) times a tile's fixed part and its steps of 256 K.  Fitted to
+    // M 200 .. 16640, N 151 .. 32000, K 256 .. 8192, where the choice costs 1% over
+    // the better one in the mean.  Measured: 2048 x 4096 x 256 8.5 us on either, x
+    // 1024 10.0 on pairs and 11.1 on single CTAs, x 4096 17.1 and 21.1; 16640 x 5120
+    // x 512 53 and 100; 1536 x 4096 x 256 8.4 and 7.4.
+    const int64_t steps = cdiv(K, kF4StepK);
+    const int64_t t_pair = cdiv(M, kF4Pair) * cdiv(N, kF4Pair), t_one = cdiv(M, 128) * cdiv(N, kF4Rows);
+    const double pair_us = 4.5 + (double)cdiv(t_pair, std::max(1, num_sms / 2)) * (1.8 + 0.31 * (double)steps);
+    const double one_us = 1.35 + (double)t_one / num_sms * (1.91 + 0.275 * (double)steps);
+    s.pair = M > 128 && t_one > num_sms && pair_us < one_us;
     s.tiles_n = (int)cdiv(N, s.pair ? kF4Pair : kF4Rows);
     // single CTAs: the narrowest tile that holds every token, and 128 columns only
     // where the tiles fill the SMs without K being split
@@ -226,7 +237,6 @@ Fp4Plan plan_fp4(int64_t M, int64_t N, int64_t K, int num_sms)
         // adding the sums (600 cycles at 16 columns, 2300 at 64: at 777 x 1000 x
         // 2080, nine steps in all, 6.0 us on one CTA per tile and 7.3 on two)
         const int64_t tiles = (int64_t)s.tiles_m * s.tiles_n;
-        const int64_t steps = cdiv(K, kF4StepK);
         const int64_t room = std::max<int64_t>(1, std::min<int64_t>(2 * num_sms / tiles, steps / (1 + s.bn / 16)));
         s.max_parts = (int)std::min<int64_t>(room, kF4MaxCluster);
         // and over clusters, where that leaves more than half of the room and 8 steps each

@@ -456,7 +456,7 @@ def _code(t: torch.Tensor, what: str) -> int:
 def _call(fn: str, dev: torch.device, *args):
     """Calls the C entry point on dev's current stream, with dev current."""
     index = dev.index
-    if dev.type != "cuda":
+    if index is None:
         raise ValueError(f"{fn}: expected CUDA tensors, got {dev}")
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
@@ -602,7 +602,10 @@ def fp8_rmsnorm_quant_1x128(x: torch.Tensor, weight: torch.Tensor, residual: Opt
     rows, cols = x.shape
     if s.shape != (rows, (cols + 127) // 128) or s.device != x.device:
         raise ValueError(f"scale_inv: expected a ({rows}, {(cols + 127) // 128}) grid on {x.device}")
-    _call("fp8_rmsnorm_quant_1x128", x.device, *args, s.data_ptr(), _grid_ld(s, rows), rule)
+    one, ld = s.stride()
+    if one != 1 or s.dtype != torch.float32 or ld < rows:
+        ld = _grid_ld(s, rows)
+    _call("fp8_rmsnorm_quant_1x128", x.device, *args, s.data_ptr(), ld, rule)
     return q, s, x if residual is None else h, rstd, y
 
 
