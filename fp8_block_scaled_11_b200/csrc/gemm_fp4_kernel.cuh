@@ -83,9 +83,11 @@ struct Fp4Cfg {
     static constexpr uint32_t w_bytes = kF4Rows * 128;      // 16 KB
     static constexpr uint32_t t_bytes = BN * 128;
     static constexpr uint32_t sf_bytes = 2 * 2 * kSfTileBytes;   // B^T's block and A's, two tiles each
-    // sums received: [rank][owned group of four columns][128 rows][4] fp32
+    // sums received: [rank][owned group of four columns][128 rows][4] fp32, in
+    // memory of their own, or for the widest tile in the stages' place (then the
+    // cluster meets once more, when all its products are done)
     static constexpr uint32_t red_bytes = (BN < 32 ? 32 : BN) * kF4Rows * 4;
-    static constexpr bool split = BN <= 64;                 // K may be split over a cluster
+    static constexpr bool red_own = BN <= 64;
     // two CTAs per SM: at most 113 KB of shared memory and 256 columns of TMEM each
     static constexpr int stages = BN <= 32 ? 4 : 3;
     static constexpr uint32_t acc_cols = BN < 32 ? 32 : BN;
@@ -95,8 +97,9 @@ struct Fp4Cfg {
     // shared memory
     static constexpr uint32_t t_off = stages * w_bytes;
     static constexpr uint32_t sf_off = t_off + stages * t_bytes;
-    static constexpr uint32_t red_off = sf_off + stages * sf_bytes;
-    static constexpr uint32_t bar_off = red_off + (split ? red_bytes : 0);
+    static constexpr uint32_t red_off = red_own ? sf_off + stages * sf_bytes : 0;
+    static constexpr uint32_t bar_off = sf_off + stages * sf_bytes + (red_own ? red_bytes : 0);
+    static_assert(red_own || red_bytes <= sf_off, "sums received exceed the stages");
     static constexpr uint32_t n_bars = 3 * stages + 2;
     static constexpr uint32_t misc_off = bar_off + n_bars * 8;
     static constexpr uint32_t alloc = misc_off + 16 + 1024;
@@ -234,7 +237,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         mbar_init(red_full, 1);
         *abort_flag = 0;
         fence_barrier_init();
-        if (C::split && parts > 1) mbar_arrive_expect_tx(red_full, (parts - 1) * owned * kQuadBytes);
+        if (parts > 1) mbar_arrive_expect_tx(red_full, (parts - 1) * owned * kQuadBytes);
         prefetch_tensormap(&tmW);
         prefetch_tensormap(&tmT);
     }
@@ -246,7 +249,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     // the peers may send once every CTA of the cluster has passed here
-    if (C::split && parts > 1) cluster_arrive();
+    if (parts > 1) cluster_arrive();
     const uint32_t tmem_base = *tmem_slot;
     // this CTA's steps: part of p.splits * parts (steps <= 2^23 and at most 256
     // parts: 32 bits hold the products)
@@ -321,7 +324,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 if (++stage == C::stages) { stage = 0; phase ^= 1u; }
             }
             if (!ok) give_up();
-            // also when nothing was issued: the epilogue, and the end of the CTA, wait for it
+            // also when nothing was issued: the epilogue and the end of the CTA wait for it
             umma_commit(tm_full);
             mbar_wait_bounded(tm_full, 0, nullptr, kDrainLimitNs);
         }
@@ -376,8 +379,12 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         float* dst32 = p.splits > 1 ? p.ws + ((int64_t)split * p.M + m0) * ld + n
                                     : static_cast<float*>(p.D) + (int64_t)m0 * ld + n;
         __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(p.D) + (int64_t)m0 * ld + n;
-        if (C::split && parts > 1) {
+        if (parts > 1) {
             cluster_wait();
+            if (!C::red_own) {
+                cluster_arrive();
+                cluster_wait();
+            }
             // slot of (rank, owned quad i): 128 rows of 16 bytes
             const uint32_t mine = sbase + C::red_off + (uint32_t)row * 16u;
             const uint32_t share = ((quads + parts - 1) >> log_parts) * kQuadBytes;
@@ -413,9 +420,13 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         }
         if (!ok && lane == 0) give_up();
     }
-    if (C::split && parts > 1 && warp < 2) {
+    if (parts > 1 && warp < 2) {
         __syncwarp();
         cluster_wait();
+        if (!C::red_own) {
+            cluster_arrive();
+            cluster_wait();
+        }
     }
     __syncwarp();
     tc_fence_before();

@@ -203,7 +203,7 @@ struct Fp4Plan {
     bool pair;                  // 256 x 256 tiles on CTA pairs; else 128 x bn tiles on single CTAs
     int bn;
     int tiles_m, tiles_n;
-    int max_parts;              // CTAs of a cluster that may share a tile's K
+    int parts;                  // CTAs of a cluster that share a tile's K
     int splits;                 // parts of K that go through the workspace
     int64_t ldw;
     size_t ws_bytes;
@@ -225,32 +225,48 @@ Fp4Plan plan_fp4(int64_t M, int64_t N, int64_t K, int num_sms)
     const double one_us = 1.35 + (double)t_one / num_sms * (1.91 + 0.275 * (double)steps);
     s.pair = M > 128 && t_one > num_sms && pair_us < one_us;
     s.tiles_n = (int)cdiv(N, s.pair ? kF4Pair : kF4Rows);
-    // single CTAs: the narrowest tile that holds every token, and 128 columns only
-    // where the tiles fill the SMs without K being split
-    s.bn = s.pair ? kF4Pair : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 || s.tiles_n * cdiv(M, 128) < num_sms ? 64 : 128;
-    s.tiles_m = (int)cdiv(M, s.bn);
-    s.max_parts = 1;
-    int splits = 1;
-    if (s.bn <= 64) {
-        // K over the CTAs of a cluster: as many as two CTAs per SM have room for,
-        // with steps enough each (256 K, about 550 cycles) to pay for sending and
-        // adding the sums (600 cycles at 16 columns, 2300 at 64: at 777 x 1000 x
-        // 2080, nine steps in all, 6.0 us on one CTA per tile and 7.3 on two)
-        const int64_t tiles = (int64_t)s.tiles_m * s.tiles_n;
-        const int64_t room = std::max<int64_t>(1, std::min<int64_t>(2 * num_sms / tiles, steps / (1 + s.bn / 16)));
-        s.max_parts = (int)std::min<int64_t>(room, kF4MaxCluster);
-        // and over clusters, where that leaves more than half of the room and 8 steps each
-        if (room >= 2 * kF4MaxCluster)
-            splits = (int)std::max<int64_t>(1, std::min<int64_t>({room / kF4MaxCluster, steps / (8 * kF4MaxCluster), 32}));
+    s.parts = 1;
+    s.splits = 1;
+    if (s.pair) {
+        s.bn = kF4Pair;
+    } else {
+        // single CTAs: the narrowest tile that holds every token, or either of the two
+        // widest ones; and K over the CTAs of a cluster where its shorter share of
+        // steps (256 K) pays for sending and adding the sums.  By what a unit takes in
+        // us, two per SM: 5120 x 8192 takes 9.0 at 72 tokens (four parts, 128 columns;
+        // one part 14.2), 13.8 at 256 (two parts, 128 columns; one 15.3, with 64
+        // columns 15.6); 1000 x 2080 5.0 at 256 (four parts, 64 columns; one 6.0), 6.2
+        // at 777 (one part, 64 columns; two 7.6, with 128 columns 7.0).
+        const int widest = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+        double best = 1e30;
+        for (int bn = std::min(widest, 64); bn <= widest; bn *= 2) {
+            const int64_t units = cdiv(M, bn) * s.tiles_n;
+            const double step = bn <= 32 ? 0.3 : bn == 64 ? 0.42 : 0.5;
+            for (int parts = 1; parts <= kF4MaxCluster; parts *= 2) {
+                if (parts > 1 && (units * parts > 2 * num_sms || steps < 2 * parts)) break;
+                double us = (double)cdiv(steps, parts) * step * (double)cdiv(units * parts, 2 * num_sms);
+                if (parts == 1) us += 0.012 * bn;
+                else us += 0.034 * bn * (units * parts > num_sms ? 1.3 : 1.0);
+                if (us < best) {
+                    best = us;
+                    s.bn = bn;
+                    s.parts = parts;
+                }
+            }
+        }
+        // very long K over clusters too, where they leave half of the room and 8 steps a CTA
+        const int64_t ctas = cdiv(M, s.bn) * s.tiles_n * s.parts;
+        if (s.parts == kF4MaxCluster)
+            s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({2 * num_sms / ctas, steps / (8 * s.parts), 32}));
     }
-    s.splits = splits;
+    s.tiles_m = (int)cdiv(M, s.bn);
     s.ldw = (N + 3) & ~int64_t(3);
-    s.ws_bytes = splits > 1 ? (size_t)splits * (size_t)M * (size_t)s.ldw * sizeof(float) : 0;
+    s.ws_bytes = s.splits > 1 ? (size_t)s.splits * (size_t)M * (size_t)s.ldw * sizeof(float) : 0;
     return s;
 }
 
 template <int BN>
-fp8bs_status launch_fp4(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap& tT, const Fp4Params& p, int max_parts,
+fp8bs_status launch_fp4(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap& tT, const Fp4Params& p, int parts,
                         cudaStream_t stream)
 {
     auto k = gemm_fp4_kernel<BN>;
@@ -283,7 +299,7 @@ fp8bs_status launch_fp4(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap&
             // counts one CTA per SM; two fit by Fp4Cfg's limits on registers,
             // shared memory and TMEM (256 CTAs in clusters of four, 24 x 8192 x
             // 5120: 5.5 us, on half as many 6.5).
-            for (int i = 1; Fp4Cfg<BN>::split && i <= 3; ++i) {
+            for (int i = 1; i <= 3; ++i) {
                 attr[0].val.clusterDim.x = 1u << i;
                 cfg.gridDim = dim3((unsigned)(d->num_sms >> i << i), 1, 1);
                 int nc = 0;
@@ -293,10 +309,10 @@ fp8bs_status launch_fp4(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap&
             d->fp4_attr_set[slot].store(true, std::memory_order_release);
         }
     }
-    // the most CTAs per tile with which all clusters are resident at once
+    // as many CTAs per tile as planned, or fewer, so that all clusters are resident at once
     int log_parts = 0;
     for (int i = 1; i <= 3; ++i)
-        if ((1 << i) <= max_parts && p.num_units <= d->fp4_clusters[slot][i].load(std::memory_order_relaxed)) log_parts = i;
+        if ((1 << i) <= parts && p.num_units <= d->fp4_clusters[slot][i].load(std::memory_order_relaxed)) log_parts = i;
     attr[0].val.clusterDim.x = 1u << log_parts;
     cfg.gridDim = dim3((unsigned)(p.num_units << log_parts), 1, 1);
     cfg.numAttrs = 2;
@@ -563,7 +579,8 @@ fp8bs_status fp4_scaled_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* A, 
     // the weights of a band (as many tiles as fit 32 MB of L2) are read once from
     // memory, A once per band: 16640 x 5120 x 8192 in one band 281 us, in bands of 8
     // of its 20 tiles 291, of 2 313 (sustained)
-    p.band = (int32_t)std::max<int64_t>(4, (int64_t)(32 << 20) / ((plan.pair ? kF4Pair : kF4Rows) * cdiv(K, 2)));
+    p.band = (int32_t)std::min<int64_t>(
+        plan.tiles_n, std::max<int64_t>(4, (int64_t)(32 << 20) / ((plan.pair ? kF4Pair : kF4Rows) * cdiv(K, 2))));
     p.num_units = (int64_t)plan.tiles_m * plan.tiles_n * plan.splits;
     p.sfa = scale_a;
     p.sfb = scale_b;
@@ -575,10 +592,10 @@ fp8bs_status fp4_scaled_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* A, 
     p.err = d->err_ptr;
     if (plan.pair) return launch_fp4_pair(d, tW, tT, p, stream);
     switch (plan.bn) {
-    case 16: st = launch_fp4<16>(d, tW, tT, p, plan.max_parts, stream); break;
-    case 32: st = launch_fp4<32>(d, tW, tT, p, plan.max_parts, stream); break;
-    case 64: st = launch_fp4<64>(d, tW, tT, p, plan.max_parts, stream); break;
-    default: st = launch_fp4<128>(d, tW, tT, p, plan.max_parts, stream); break;
+    case 16: st = launch_fp4<16>(d, tW, tT, p, plan.parts, stream); break;
+    case 32: st = launch_fp4<32>(d, tW, tT, p, plan.parts, stream); break;
+    case 64: st = launch_fp4<64>(d, tW, tT, p, plan.parts, stream); break;
+    default: st = launch_fp4<128>(d, tW, tT, p, plan.parts, stream); break;
     }
     if (st != FP8BS_OK || plan.splits == 1) return st;
     const int vec_out = aligned16(D) && (ldd * (int64_t)dtype_size(out_dtype)) % 16 == 0;
