@@ -410,7 +410,7 @@ def _mat(t: torch.Tensor, shape, dtype, dev, what: str):
     ld, one = t.stride()
     if one != 1:
         raise ValueError(f"{what}: expected a row-major matrix (unit column stride)")
-    return t.data_ptr(), ld
+    return t.data_ptr(), ld if shape[0] != 1 else shape[1]      # one row: any stride will do
 
 
 def _vec(t: torch.Tensor, n: int, dev, what: str) -> int:
@@ -488,7 +488,7 @@ def _codes(q: torch.Tensor, what: str):
     ld, one = q.stride()
     if one != 1:
         raise ValueError(f"{what}: expected a row-major matrix (unit column stride)")
-    return rows, 2 * half, q.data_ptr(), ld
+    return rows, 2 * half, q.data_ptr(), ld if rows != 1 else half
 
 
 def fp4_quant_1x32(x: torch.Tensor, transpose_out: bool = False, q: Optional[torch.Tensor] = None,

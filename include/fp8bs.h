@@ -440,7 +440,8 @@ fp8bs_status fp8_scaled_gemm_grouped(int64_t groups, const int64_t* group_rows, 
  * x, residual, weight, h, y, q and the scales 16-byte aligned, rstd 4-byte;
  * leading dims in bytes multiples of 16; ld_scale % 4 == 0.  eps >= 0; eps = 0
  * with an all-zero row divides by zero.  Inputs must be finite, and a row's sum
- * of squares must fit fp32.  Errors as the quantizations.
+ * of squares and its y must fit fp32.  Other than h, no output may overlap an
+ * input or another output.  Errors as the quantizations.
  */
 fp8bs_status fp8_rmsnorm_quant_1x128(const void* x, int64_t ldx, const void* residual, int64_t ld_res, fp8bs_dtype xt,
                                      int64_t rows, int64_t cols, const void* weight, fp8bs_dtype wt, float eps,
@@ -524,14 +525,16 @@ fp8bs_status fp4_dequant_1x32(const uint8_t* q, int64_t ldq, const uint8_t* scal
  * A, scale_a   M x K codes, leading dim lda bytes, and their scale tiles
  *              (fp4_quant_1x32, fp4_rmsnorm_quant_1x32).
  * Bt, scale_b  N x K codes, leading dim ldb bytes, and their scale tiles.
- *              A scale byte of 255 is NaN, as in the format.
+ *              A scale byte of 255 is NaN, as in the format: it makes its row of
+ *              A (of Bt) NaN in all of D.  The bytes of groups past K in a row's
+ *              last four take part (with zeros): 255 there is NaN too.
  * D            M x N, dtype out_dtype (bf16 rounded to nearest even, or fp32),
  *              leading dim ldd elements; any ldd >= N.
- * workspace    optional fp32 scratch for split-K (used when the output has few
- *              tiles): NULL/0 to disable split-K, or at least
- *              fp4_scaled_gemm_workspace_size(M, N, K) bytes, 16-byte aligned.
- *              Partial sums are added in a fixed order: results are
- *              deterministic.  Calls that may overlap on the GPU need a
+ * workspace    optional fp32 scratch for very long K and few tiles, which is split
+ *              beyond what a cluster of CTAs shares: NULL/0 to do without, or at
+ *              least fp4_scaled_gemm_workspace_size(M, N, K) bytes (0 for most
+ *              sizes), 16-byte aligned.  Partial sums are added in a fixed order:
+ *              results are deterministic on one kind of device.  Calls that may overlap on the GPU need a
  *              workspace each.
  * Any M, N >= 1; K >= 32, K % 32 == 0.  A, Bt, scale_a, scale_b 16-byte aligned;
  * lda, ldb multiples of 16; D aligned to its element size.

@@ -139,7 +139,8 @@ def check(got, a, b, out_dtype, k, splits=64):
 SHAPES = [(1, 1, 32), (1, 5120, 8192), (7, 130, 96), (16, 128, 256), (17, 1000, 288), (33, 257, 4128), (64, 512, 512),
           (65, 300, 160), (128, 128, 2048), (129, 384, 1056), (200, 640, 224), (256, 4096, 1024), (300, 1000, 2080),
           (777, 1000, 2080), (1024, 19000, 64), (129, 19000, 96), (2300, 2304, 288),
-          (5000, 1100, 544), (2305, 2050, 4128), (70, 19000, 160)]
+          (5000, 1100, 544), (2305, 2050, 4128), (70, 19000, 160), (1, 100, 1056), (5, 100, 2080), (20, 130, 2080),
+          (40, 100, 2080), (65, 100, 4128), (500, 520, 8224), (4000, 2050, 96)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -166,9 +167,13 @@ def test_product_exact(M, N, K):
     assert torch.equal(d, d2)
 
 
-@pytest.mark.parametrize("M,N,K", [(5000, 4200, 8192), (16640, 1300, 4128), (300, 40000, 1600)])
+@pytest.mark.parametrize("M,N,K", [(5000, 4200, 8192), (16640, 1300, 4128), (300, 40000, 1600), (65, 5000, 3104),
+                                   (65, 5000, 12320), (529, 2050, 8224), (500, 520, 32800), (24, 100, 65568),
+                                   (2048, 4096, 1056), (2600, 4100, 32), (1600, 5200, 4160)])
 def test_product_exact_large(M, N, K):
-    """Many tiles per CTA and many steps per tile, the reference in 64 bits on the GPU: exact as above."""
+    """Many tiles per CTA, many steps per tile, K split over clusters of two, four and eight CTAs at every tile width
+    and through the workspace; the reference in 64 bits on the GPU: exact as above."""
+    assert 36 * K < 2 ** 22
     a, sa, av = operand(M, K, 51, spread=0)
     b, sb, bv = operand(N, K, 52, spread=0)
     want = (torch.from_numpy(av).cuda() @ torch.from_numpy(bv).cuda().t())
@@ -194,6 +199,25 @@ def test_product_strides_and_guards(M, N, K, ldd, dtype):
     no_device_error()
     check(buf[:M, :N], av, bv, DT[dtype], K)
     assert bool((buf[:M, N:] == -7.0).all()) and bool((buf[M:] == -7.0).all())
+
+
+def test_one_row_with_any_stride():
+    """One token taken out of a larger tensor, and a row whose stride is meaningless."""
+    N, K = 300, 512
+    big, sbig, bv = operand(9, K, 61)
+    b, sb, bw = operand(N, K, 62)
+    q = torch.as_strided(big, (1, K // 2), (1, 1), 4 * (K // 2))       # row 4
+    x = ops.fp4_dequant_1x32(big, sbig)[4:5]
+    qa, sa = ops.fp4_quant_1x32(x)                                      # the same values again
+    va = ops.fp4_dequant_1x32(qa, sa, out_dtype=torch.float32)
+    assert torch.equal(va, x.float())
+    d = ops.fp4_scaled_gemm(torch.as_strided(qa, (1, K // 2), (3, 1)), b, sa, sb, out_dtype=torch.float32)
+    check(d, bv[4:5], bw, torch.float32, K)
+    s4 = ops.fp4_scale_tiles(1, K, "cuda")
+    s4[0, :, 0, 0] = sbig[0, :, 4, 0]
+    d = ops.fp4_scaled_gemm(q, b, s4, sb, out_dtype=torch.float32)
+    no_device_error()
+    check(d, bv[4:5], bw, torch.float32, K)
 
 
 def test_product_nan_scale_stays_in_its_row():
