@@ -53,8 +53,8 @@ RowShape row_shape(int64_t eights, int64_t max_tx, const int (&order)[3])
     return best;
 }
 
-template <typename T, int BITS>
-fp8bs_status launch_norm(DeviceInfo* d, const NormParams& p, cudaStream_t stream)
+template <typename T, typename W, int BITS>
+fp8bs_status launch_norm_rows(DeviceInfo* d, const NormParams& p, cudaStream_t stream)
 {
     const int64_t eights = cdiv(p.cols, 8);
     // one eight per thread where few rows would leave the GPU idle otherwise (a
@@ -69,10 +69,22 @@ fp8bs_status launch_norm(DeviceInfo* d, const NormParams& p, cudaStream_t stream
     const int ty = (int)std::max<int64_t>(1, std::min<int64_t>({256 / sh.tx, p.rows, sh.tx > 32 ? 8 : 16}));
     const dim3 block((unsigned)sh.tx, (unsigned)(sh.tx == 16 ? (ty + 1) / 2 * 2 : ty));
     const unsigned grid = (unsigned)cdiv(p.rows, block.y);
-    if (sh.vpt == 1) rmsnorm_quant_kernel<T, BITS, 1><<<grid, block, 0, stream>>>(p);
-    else if (sh.vpt == 2) rmsnorm_quant_kernel<T, BITS, 2><<<grid, block, 0, stream>>>(p);
-    else rmsnorm_quant_kernel<T, BITS, 4><<<grid, block, 0, stream>>>(p);
+    const bool full = p.cols == 8 * (int64_t)sh.vpt * sh.tx && p.rows % block.y == 0;
+    if (sh.vpt == 1) rmsnorm_quant_kernel<T, W, BITS, 1, false><<<grid, block, 0, stream>>>(p);
+    else if (sh.vpt == 2) rmsnorm_quant_kernel<T, W, BITS, 2, false><<<grid, block, 0, stream>>>(p);
+    else if (!full) rmsnorm_quant_kernel<T, W, BITS, 4, false><<<grid, block, 0, stream>>>(p);
+    else rmsnorm_quant_kernel<T, W, BITS, 4, true><<<grid, block, 0, stream>>>(p);
     return launch_status();
+}
+
+template <int BITS>
+fp8bs_status launch_norm(DeviceInfo* d, const NormParams& p, fp8bs_dtype xt, cudaStream_t stream)
+{
+    if (xt == FP8BS_BF16)
+        return p.w_f32 ? launch_norm_rows<__nv_bfloat16, float, BITS>(d, p, stream)
+                       : launch_norm_rows<__nv_bfloat16, __nv_bfloat16, BITS>(d, p, stream);
+    return p.w_f32 ? launch_norm_rows<float, float, BITS>(d, p, stream)
+                   : launch_norm_rows<float, __nv_bfloat16, BITS>(d, p, stream);
 }
 
 // The backward's launch and the bytes of its workspace.  Rows are read once, over
@@ -406,7 +418,7 @@ fp8bs_status fp8_rmsnorm_quant_1x128(const void* x, int64_t ldx, const void* res
     if (cols % 16 || ld_scale % 4) return FP8BS_ERR_ALIGNMENT;
     DeviceInfo* d = nullptr;
     if ((st = get_device(&d)) != FP8BS_OK) return st;
-    return xt == FP8BS_BF16 ? launch_norm<__nv_bfloat16, 8>(d, p, stream) : launch_norm<float, 8>(d, p, stream);
+    return launch_norm<8>(d, p, xt, stream);
 }
 
 fp8bs_status fp4_rmsnorm_quant_1x32(const void* x, int64_t ldx, const void* residual, int64_t ld_res, fp8bs_dtype xt,
@@ -422,7 +434,7 @@ fp8bs_status fp4_rmsnorm_quant_1x32(const void* x, int64_t ldx, const void* resi
     if (ldq < cols / 2) return FP8BS_ERR_INVALID_ARG;
     DeviceInfo* d = nullptr;
     if ((st = get_device(&d)) != FP8BS_OK) return st;
-    return xt == FP8BS_BF16 ? launch_norm<__nv_bfloat16, 4>(d, p, stream) : launch_norm<float, 4>(d, p, stream);
+    return launch_norm<4>(d, p, xt, stream);
 }
 
 size_t fp8bs_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols)

@@ -112,18 +112,27 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const Eight& e)
                                               cvt_bf16x2(e.v[2].x, e.v[2].y), cvt_bf16x2(e.v[3].x, e.v[3].y));
 }
 
+// Eight weights (read-only, reused by every row).
+__device__ __forceinline__ void load_ro(Vec8<__nv_bfloat16>& v, const __nv_bfloat16* p)
+{
+    v.raw = __ldg(reinterpret_cast<const uint4*>(p));
+}
+__device__ __forceinline__ void load_ro(Vec8<float>& v, const float* p)
+{
+    v.a = __ldg(reinterpret_cast<const float4*>(p));
+    v.b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+}
+
 // Eight weights as fp32 (bf16 or fp32 in memory).
 __device__ __forceinline__ Eight load_weight8(const void* w, int w_f32, int64_t c)
 {
     if (w_f32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c);
         Vec8<float> v;
-        v.a = __ldg(p);
-        v.b = __ldg(p + 1);
+        load_ro(v, static_cast<const float*>(w) + c);
         return eight_of(v);
     }
     Vec8<__nv_bfloat16> v;
-    v.raw = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + c));
+    load_ro(v, static_cast<const __nv_bfloat16*>(w) + c);
     return eight_of(v);
 }
 
@@ -235,10 +244,12 @@ __device__ __forceinline__ int share_lane(int i)
 // VPT eights of normalised values of row r, columns (i tx + x) 8 .. + 7 (zero past
 // the last column): quantised and stored with their groups' scales.  Whole warps
 // take part; 16 neighbouring lanes (4 for the groups of 32) hold a group.
-template <int BITS, int VPT>
+// FULL: every eight is inside the matrix.
+template <int BITS, int VPT, bool FULL>
 __device__ __forceinline__ void quantise_store(const NormParams& p, int64_t r, bool row_ok, int tx, int x,
                                                const Eight (&y)[VPT])
 {
+    auto inside = [&](int c) { return FULL || (row_ok && c < p.cols); };
     const int lane = threadIdx.x + threadIdx.y * blockDim.x & 31;
     float m[VPT];
 #pragma unroll
@@ -249,13 +260,13 @@ __device__ __forceinline__ void quantise_store(const NormParams& p, int64_t r, b
         const int mi = share_index<VPT, 8>(lane);
         const int mc = (mi * tx + (x & ~15)) * 8;               // first column of the lane's own group
         const int own = VPT == 4 ? 3 : VPT == 2 ? 7 : 15;       // one of the lanes that hold the same group
-        if ((lane & own) == 0 && row_ok && mc < p.cols) static_cast<float*>(p.scale)[r + (mc >> 7) * p.lds] = __frcp_rn(mine);
+        if ((lane & own) == 0 && inside(mc)) static_cast<float*>(p.scale)[r + (mc >> 7) * p.lds] = __frcp_rn(mine);
         uint8_t* q = p.q + r * p.ldq;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const float s = VPT == 1 ? mine : __shfl_sync(0xffffffffu, mine, (lane & 16) + share_lane<VPT, 8>(i));
             const int c = (i * tx + x) * 8;
-            if (row_ok && c < p.cols) {
+            if (inside(c)) {
                 const float2 k = make_float2(s, s);
                 float2 t[4];
 #pragma unroll
@@ -271,17 +282,17 @@ __device__ __forceinline__ void quantise_store(const NormParams& p, int64_t r, b
         const int mi = share_index<VPT, 2>(lane);
         // the chunk's word: its four groups' bytes, groups past the last column 127
         const int mc = (mi * tx + (x & ~3)) * 8;
-        const uint32_t word = sf_gather_word(mc < p.cols ? mine : 127u, lane);
+        const uint32_t word = sf_gather_word(FULL || mc < p.cols ? mine : 127u, lane);
         const int own = VPT == 4 ? 12 : VPT == 2 ? 13 : 15;
         const int chunk = (mi * tx + (x & ~15)) * 8;
-        if ((lane & own) == 0 && row_ok && chunk < p.cols)
+        if ((lane & own) == 0 && inside(chunk))
             *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.scale) + sf_word_offset(r, chunk >> 7, p.lds)) = word;
         uint8_t* q = p.q + r * p.ldq;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const uint32_t byte = VPT == 1 ? mine : __shfl_sync(0xffffffffu, mine, (lane & 28) + share_lane<VPT, 2>(i));
             const int c = (i * tx + x) * 8;
-            if (row_ok && c < p.cols) {
+            if (inside(c)) {
                 const float f[8] = {y[i].v[0].x, y[i].v[0].y, y[i].v[1].x, y[i].v[1].y,
                                     y[i].v[2].x, y[i].v[2].y, y[i].v[3].x, y[i].v[3].y};
                 *reinterpret_cast<uint32_t*>(q + (c >> 1)) = mx4_pack8(f, mx4_inv_scale(byte));
@@ -295,36 +306,45 @@ __device__ __forceinline__ void quantise_store(const NormParams& p, int64_t r, b
 // registers between the sum of squares and the quantisation, so memory is read
 // once.  Row blockIdx.x * blockDim.y + threadIdx.y; thread t holds the eights
 // t, t + blockDim.x, ... of the row, so that 16 neighbouring lanes hold a group
-// of 128.
+// of 128.  FULL: the threads cover the rows and columns exactly, nothing is tested.
 // --------------------------------------------------------------------------
-template <typename T, int BITS, int VPT>
+template <typename T, typename W, int BITS, int VPT, bool FULL>
 __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_quant_kernel(const NormParams p)
 {
     const int tx = blockDim.x, x = threadIdx.x;
     const int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const bool row_ok = r < p.rows;
-    const T* src = static_cast<const T*>(p.x) + r * p.ldx;
-    const T* res = static_cast<const T*>(p.res) + r * p.ldr;
-    Vec8<T> a[VPT], b[VPT];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = (i * tx + x) * 8;
-        const bool ok = row_ok && c < p.cols;
-        a[i].zero();
-        b[i].zero();
-        if (ok) a[i].load(src + c);
-        if (ok && p.res != nullptr) b[i].load(res + c);
-    }
+    const bool row_ok = FULL || r < p.rows;
+    auto inside = [&](int c) { return FULL || (row_ok && c < p.cols); };
+    Vec8<T> a[VPT];
     float ss = 0.f;
+    {
+        const T* src = static_cast<const T*>(p.x) + r * p.ldx;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = (i * tx + x) * 8;
-        if (p.res != nullptr) {
-            add_round(a[i], b[i]);
-            if (row_ok && c < p.cols) store_vec(static_cast<T*>(p.h) + r * p.ldh + c, a[i]);
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (i * tx + x) * 8;
+            if (!FULL) a[i].zero();
+            if (inside(c)) a[i].load(src + c);
         }
-        ss = sum_squares(eight_of(a[i]), ss);
     }
+    if (p.res != nullptr) {
+        const T* res = static_cast<const T*>(p.res) + r * p.ldr;
+        T* h = static_cast<T*>(p.h) + r * p.ldh;
+        Vec8<T> b[VPT];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (i * tx + x) * 8;
+            if (!FULL) b[i].zero();
+            if (inside(c)) b[i].load(res + c);
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (i * tx + x) * 8;
+            add_round(a[i], b[i]);
+            if (inside(c)) store_vec(h + c, a[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) ss = sum_squares(eight_of(a[i]), ss);
     ss = row_sum(ss);
     const float rstd = rstd_of(ss, p.inv_cols, p.eps);
     if (row_ok && x == 0 && p.rstd != nullptr) p.rstd[r] = rstd;
@@ -332,13 +352,18 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_quant_kernel(co
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (i * tx + x) * 8;
-        y[i] = eight_zero();
-        if (row_ok && c < p.cols) {
-            y[i] = normalise(eight_of(a[i]), rstd, load_weight8(p.w, p.w_f32, c));
-            if (p.y != nullptr) store8(static_cast<T*>(p.y) + r * p.ldy + c, y[i]);
-        }
+        Vec8<W> w;
+        if (!FULL) w.zero();
+        if (inside(c)) load_ro(w, static_cast<const W*>(p.w) + c);
+        y[i] = normalise(eight_of(a[i]), rstd, eight_of(w));
     }
-    quantise_store<BITS, VPT>(p, r, row_ok, tx, x, y);
+    if (p.y != nullptr) {
+        T* dst = static_cast<T*>(p.y) + r * p.ldy;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (inside((i * tx + x) * 8)) store8(dst + (i * tx + x) * 8, y[i]);
+    }
+    quantise_store<BITS, VPT, FULL>(p, r, row_ok, tx, x, y);
 }
 
 // --------------------------------------------------------------------------
@@ -520,7 +545,7 @@ __global__ void __launch_bounds__(512) rmsnorm_quant_wide_kernel(const NormParam
             y[0] = normalise(eight_of(a), rstd, load_weight8(p.w, p.w_f32, c));
             if (p.y != nullptr) store8(static_cast<T*>(p.y) + r * p.ldy + c, y[0]);
         }
-        quantise_store<BITS, 1>(p, r, true, 0, (int)(c >> 3), y);
+        quantise_store<BITS, 1, false>(p, r, true, 0, (int)(c >> 3), y);
     }
 }
 
