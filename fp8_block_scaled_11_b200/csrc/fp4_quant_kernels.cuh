@@ -21,9 +21,9 @@ __device__ __forceinline__ uint32_t sf_gather_word(uint32_t byte, int lane)
 }
 
 // Largest magnitude over the four lanes that share a group of 32 values.
-__device__ __forceinline__ float group32_absmax(const float (&f)[8])
+__device__ __forceinline__ float group32_absmax(const Eight& e)
 {
-    float m = absmax8(f);
+    float m = absmax(e);
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
@@ -32,45 +32,48 @@ __device__ __forceinline__ float group32_absmax(const float (&f)[8])
 // Groups along the columns.  A CTA owns a scale tile's 128 rows x 128 columns;
 // half-warp h of 16 takes rows h, h + 16 (mod 32) of each of the four 32-row
 // quarters, whose scale words are adjacent in the tile (one 16-byte store).
+// FULL: rows and columns are multiples of 128, nothing is tested.
 // --------------------------------------------------------------------------
-template <typename T>
+template <typename T, bool FULL>
 __global__ void __launch_bounds__(256) fp4_quant_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
                                                              int64_t ldx, uint8_t* __restrict__ q, int64_t ldq,
-                                                             uint8_t* __restrict__ sf, int64_t kcs)
+                                                             uint8_t* __restrict__ sf, int kcs)
 {
     const int lane = threadIdx.x & 31;
     const int hw = threadIdx.x >> 4;
-    const int64_t rb = blockIdx.x / kcs, kc = blockIdx.x - rb * kcs;
-    const int64_t c = kc * 128 + (threadIdx.x & 15) * 8;
-    const bool col_ok = c < cols;           // cols % 32 == 0: a group is all in or all out
+    const int rb = (int)blockIdx.x / kcs, kc = (int)blockIdx.x - rb * kcs;
+    const int64_t c = (int64_t)kc * 128 + (threadIdx.x & 15) * 8;
+    const bool col_ok = FULL || c < cols;       // cols % 32 == 0: a group is all in or all out
+    const int64_t r0 = (int64_t)rb * 128 + hw;
+    const T* src = x + r0 * ldx + c;
+    uint8_t* dst = q + r0 * ldq + (c >> 1);
+    uint8_t* scales = sf + ((int64_t)rb * kcs + kc) * (int64_t)kSfTileBytes + hw * 16;
+    // row 16 i + 32 j past r0
+    auto row_ok = [&](int i, int j) { return FULL || (col_ok && r0 + 16 * i + 32 * j < rows); };
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int64_t r0 = rb * 128 + hw + 16 * i;
         Vec8<T> v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (col_ok && r0 + 32 * j < rows) v[j].load(x + (r0 + 32 * j) * ldx + c);
-            else v[j].zero();
+            if (!FULL) v[j].zero();
+            if (row_ok(i, j)) v[j].load(src + (16 * i + 32 * j) * ldx);
         }
         uint32_t word[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float f[8];
-            v[j].get(f);
-            const uint32_t byte = mx4_scale_byte(group32_absmax(f));
-            const uint32_t codes = mx4_pack8(f, mx4_inv_scale(byte));
-            if (col_ok && r0 + 32 * j < rows) *reinterpret_cast<uint32_t*>(q + (r0 + 32 * j) * ldq + (c >> 1)) = codes;
+            const Eight e = eight_of(v[j]);
+            const uint32_t byte = mx4_scale_byte(group32_absmax(e));
+            if (row_ok(i, j)) *reinterpret_cast<uint32_t*>(dst + (16 * i + 32 * j) * ldq) = mx4_pack8(e, mx4_inv_scale(byte));
             word[j] = sf_gather_word(col_ok ? byte : 127u, lane);
         }
         // rows past the last one keep their bytes
         if ((lane & 15) == 0) {
-            uint8_t* dst = sf + sf_word_offset(r0, kc, kcs);
-            if (r0 + 96 < rows) {
-                *reinterpret_cast<uint4*>(dst) = make_uint4(word[0], word[1], word[2], word[3]);
+            if (FULL || r0 + 16 * i + 96 < rows) {
+                *reinterpret_cast<uint4*>(scales + 256 * i) = make_uint4(word[0], word[1], word[2], word[3]);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (r0 + 32 * j < rows) *reinterpret_cast<uint32_t*>(dst + 4 * j) = word[j];
+                    if (r0 + 16 * i + 32 * j < rows) *reinterpret_cast<uint32_t*>(scales + 256 * i + 4 * j) = word[j];
             }
         }
     }
@@ -83,26 +86,28 @@ __global__ void __launch_bounds__(256) fp4_quant_rows_kernel(const T* __restrict
 // blocks: warp w covers rows 32 w .. + 31, i.e. one group of each column.  The
 // codes pass through shared memory to leave in whole 16-byte pieces; its pieces
 // are permuted by the column's strip, so that a warp's words fall into 32 banks.
+// FULL: whole tiles only, nothing is tested.
 // --------------------------------------------------------------------------
 constexpr int kQ4Rows = 256, kQ4Cols = 64;
 
-template <typename T>
+template <typename T, bool FULL>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) fp4_quant_cols_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
                                                              int64_t ldx, uint8_t* __restrict__ q, int64_t ldq,
-                                                             uint8_t* __restrict__ sf, int64_t kcs, int64_t tiles_c)
+                                                             uint8_t* __restrict__ sf, int kcs, int tiles_c)
 {
     __shared__ __align__(16) uint8_t s_q[kQ4Cols * 128];
     __shared__ __align__(16) uint8_t s_sf[kQ4Cols * 8];
-    const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
+    const int tr = (int)blockIdx.x / tiles_c, tc = (int)blockIdx.x - tr * tiles_c;
     const int w = threadIdx.x >> 5, strip = threadIdx.x & 7, part = (threadIdx.x >> 3) & 3;
-    const int64_t r0 = tr * kQ4Rows + w * 32 + part * 8;
-    const int64_t c0 = tc * kQ4Cols + strip * 8;
-    const bool ok = r0 < rows && c0 < cols;     // rows % 32 == 0, cols % 16 == 0
+    const int64_t r0 = (int64_t)tr * kQ4Rows + w * 32 + part * 8;
+    const int64_t c0 = (int64_t)tc * kQ4Cols + strip * 8;
+    const bool ok = FULL || (r0 < rows && c0 < cols);     // rows % 32 == 0, cols % 16 == 0
     Block8x8<T> b;
+    const T* src = x + r0 * ldx + c0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (ok) b.row[i].load(x + (r0 + i) * ldx + c0);
-        else b.row[i].zero();
+    for (int i = 0; i < 8; ++i, src += ldx) {
+        if (!FULL) b.row[i].zero();
+        if (ok) b.row[i].load(src);
     }
     float m[8];
     b.col_absmax(m);
@@ -114,31 +119,32 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) fp4_quant_cols_ke
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const uint32_t byte = mx4_scale_byte(m[j]);
-        float f[8];
+        Eight e;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float g[8];
-            b.row[i].get(g);
-            f[i] = g[j];
+        for (int i = 0; i < 4; ++i) {
+            float g[8], h[8];
+            b.row[2 * i].get(g);
+            b.row[2 * i + 1].get(h);
+            e.v[i] = make_float2(g[j], h[j]);
         }
         const int row = strip * 8 + j;
-        *reinterpret_cast<uint32_t*>(s_q + row * 128 + ((w ^ strip) * 16) + part * 4) = mx4_pack8(f, mx4_inv_scale(byte));
+        *reinterpret_cast<uint32_t*>(s_q + row * 128 + ((w ^ strip) * 16) + part * 4) = mx4_pack8(e, mx4_inv_scale(byte));
         // (rows past x's last: a scale of one)
-        if (part == 0) s_sf[row * 8 + w] = (uint8_t)(r0 < rows ? byte : 127u);
+        if (part == 0) s_sf[row * 8 + w] = (uint8_t)(FULL || r0 < rows ? byte : 127u);
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int row = (threadIdx.x >> 3) + 32 * i, piece = threadIdx.x & 7;
-        const int64_t c = tc * kQ4Cols + row, r = tr * kQ4Rows + piece * 32;
-        if (c < cols && r < rows)
+        const int64_t c = (int64_t)tc * kQ4Cols + row, r = (int64_t)tr * kQ4Rows + piece * 32;
+        if (FULL || (c < cols && r < rows))
             *reinterpret_cast<uint4*>(q + c * ldq + (r >> 1)) =
                 *reinterpret_cast<const uint4*>(s_q + row * 128 + ((piece ^ (row >> 3)) * 16));
     }
     if (threadIdx.x < 2 * kQ4Cols) {
         const int row = threadIdx.x >> 1, half = threadIdx.x & 1;
-        const int64_t c = tc * kQ4Cols + row, kc = tr * 2 + half;
-        if (c < cols && kc < kcs)
+        const int64_t c = (int64_t)tc * kQ4Cols + row, kc = (int64_t)tr * 2 + half;
+        if (FULL || (c < cols && kc < kcs))
             *reinterpret_cast<uint32_t*>(sf + sf_word_offset(c, kc, kcs)) =
                 *reinterpret_cast<const uint32_t*>(s_sf + row * 8 + half * 4);
     }
@@ -149,46 +155,49 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) fp4_quant_cols_ke
 // outside the output type's range rounds as the type does.  The same partition as
 // fp4_quant_rows_kernel: a CTA owns a scale tile.
 // --------------------------------------------------------------------------
-template <typename T>
+template <typename T, bool FULL>
 __global__ void __launch_bounds__(256) fp4_dequant_kernel(const uint8_t* __restrict__ q, int64_t ldq,
                                                           const uint8_t* __restrict__ sf, int64_t rows, int64_t cols,
-                                                          int64_t kcs, T* __restrict__ out, int64_t ldo)
+                                                          int kcs, T* __restrict__ out, int64_t ldo)
 {
     const int hw = threadIdx.x >> 4;
-    const int64_t rb = blockIdx.x / kcs, kc = blockIdx.x - rb * kcs;
-    const int64_t c = kc * 128 + (threadIdx.x & 15) * 8;
-    if (c >= cols) return;                       // cols % 32 == 0: a group is all in or all out
-    const int group = (threadIdx.x >> 2) & 3;
+    const int rb = (int)blockIdx.x / kcs, kc = (int)blockIdx.x - rb * kcs;
+    const int64_t c = (int64_t)kc * 128 + (threadIdx.x & 15) * 8;
+    if (!FULL && c >= cols) return;              // cols % 32 == 0: a group is all in or all out
     // bf16: a lane's eight codes make 16 bytes.  fp32: a pair of lanes takes its
     // sixteen codes four at a time in turn, so that a pair stores 32 bytes in a row.
     constexpr bool kWide = sizeof(T) == 4;
     const int odd = threadIdx.x & 1;
+    const int64_t r0 = (int64_t)rb * 128 + hw;
+    const uint8_t* src = q + r0 * ldq + ((kWide ? c - odd * 8 : c) >> 1);
+    // the scale bytes of rows r0 + 16 i + 32 j: one 16-byte row of the tile each i
+    const uint8_t* scales = sf + ((int64_t)rb * kcs + kc) * (int64_t)kSfTileBytes + hw * 16 + ((threadIdx.x >> 2) & 3);
+    T* dst = out + r0 * ldo + (kWide ? c - odd * 4 : c);
     uint32_t w[8], byte[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int64_t r = rb * 128 + hw + 16 * (i & 1) + 32 * (i >> 1);
-        if (r < rows) {
+        const int dr = 16 * (i & 1) + 32 * (i >> 1);
+        if (FULL || r0 + dr < rows) {
             if constexpr (kWide) {
-                const uint2 v = __ldcs(reinterpret_cast<const uint2*>(q + r * ldq + ((c - odd * 8) >> 1)));
+                const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src + dr * ldq));
                 w[i] = __byte_perm(v.x, v.y, odd ? 0x7632 : 0x5410);
             } else {
-                w[i] = __ldcs(reinterpret_cast<const uint32_t*>(q + r * ldq + (c >> 1)));
+                w[i] = __ldcs(reinterpret_cast<const uint32_t*>(src + dr * ldq));
             }
-            byte[i] = sf[sf_word_offset(r, kc, kcs) + group];
+            byte[i] = scales[256 * (i & 1) + 4 * (i >> 1)];
         }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int64_t r = rb * 128 + hw + 16 * (i & 1) + 32 * (i >> 1);
-        if (r < rows) {
+        const int dr = 16 * (i & 1) + 32 * (i >> 1);
+        if (FULL || r0 + dr < rows) {
             float f[8];
             mx4_unpack8(w[i], mx4_scale_value(byte[i]), f);
             if constexpr (kWide) {
-                T* dst = out + r * ldo + (c - odd * 4);
-                __stcs(reinterpret_cast<float4*>(dst), make_float4(f[0], f[1], f[2], f[3]));
-                __stcs(reinterpret_cast<float4*>(dst + 8), make_float4(f[4], f[5], f[6], f[7]));
+                __stcs(reinterpret_cast<float4*>(dst + dr * ldo), make_float4(f[0], f[1], f[2], f[3]));
+                __stcs(reinterpret_cast<float4*>(dst + dr * ldo + 8), make_float4(f[4], f[5], f[6], f[7]));
             } else {
-                __stcs(reinterpret_cast<uint4*>(out + r * ldo + c),
+                __stcs(reinterpret_cast<uint4*>(dst + dr * ldo),
                        make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]),
                                   cvt_bf16x2(f[6], f[7])));
             }

@@ -18,6 +18,7 @@
 #include <cstdint>
 #include <cuda_fp16.h>
 #include "ptx.cuh"
+#include "quant_kernels.cuh"
 
 namespace fp8bs {
 
@@ -42,9 +43,51 @@ __device__ __forceinline__ float mx4_scale_value(uint32_t byte)
     return __uint_as_float(byte == 255u ? 0x7FFFFFFFu : byte == 0u ? 0x400000u : byte << 23);
 }
 
-// Eight values times s -> eight codes, value 0 in the lowest four bits.
-__device__ __forceinline__ uint32_t mx4_pack8(const float (&f)[8], float s)
+// Eight values as four fp32 pairs: the arithmetic is packed (two lanes an instruction),
+// since the quantising kernels in bf16 come close to the issue rate before they
+// reach the memory's.
+struct Eight {
+    float2 v[4];
+};
+
+template <typename T>
+__device__ __forceinline__ Eight eight_of(const Vec8<T>& a)
 {
+    Eight e;
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t w[4] = {a.raw.x, a.raw.y, a.raw.z, a.raw.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e.v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    } else {
+        e.v[0] = make_float2(a.a.x, a.a.y);
+        e.v[1] = make_float2(a.a.z, a.a.w);
+        e.v[2] = make_float2(a.b.x, a.b.y);
+        e.v[3] = make_float2(a.b.z, a.b.w);
+    }
+    return e;
+}
+
+__device__ __forceinline__ Eight eight_zero()
+{
+    Eight e;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e.v[i] = make_float2(0.f, 0.f);
+    return e;
+}
+
+__device__ __forceinline__ float absmax(const Eight& e)
+{
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(fmaxf(m, fabsf(e.v[i].x)), fabsf(e.v[i].y));
+    return m;
+}
+
+// Eight values times s -> eight codes, value 0 in the lowest four bits.
+__device__ __forceinline__ uint32_t mx4_pack8(const Eight& e, float s)
+{
+    const float2 k = make_float2(s, s);
+    const float2 a = fmul2(e.v[0], k), b = fmul2(e.v[1], k), c = fmul2(e.v[2], k), d = fmul2(e.v[3], k);
     uint32_t r;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -53,8 +96,7 @@ __device__ __forceinline__ uint32_t mx4_pack8(const float (&f)[8], float s)
         "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
         "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
         : "=r"(r)
-        : "f"(f[0] * s), "f"(f[1] * s), "f"(f[2] * s), "f"(f[3] * s), "f"(f[4] * s), "f"(f[5] * s), "f"(f[6] * s),
-          "f"(f[7] * s));
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
     return r;
 }
 

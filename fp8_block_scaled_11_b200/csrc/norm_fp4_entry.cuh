@@ -502,19 +502,23 @@ fp8bs_status fp4_quant_1x32(const void* x, fp8bs_dtype xt, int64_t rows, int64_t
     const int64_t tiles_c = transpose_out ? cdiv(cols, kQ4Cols) : kcs;
     const int64_t tiles = tiles_c * cdiv(rows, transpose_out ? kQ4Rows : 128);
     if (tiles > INT32_MAX) return FP8BS_ERR_INVALID_ARG;
-    const unsigned grid = (unsigned)tiles;
-    const __nv_bfloat16* x16 = static_cast<const __nv_bfloat16*>(x);
-    const float* x32 = static_cast<const float*>(x);
-    if (!transpose_out) {
-        if (xt == FP8BS_BF16)
-            fp4_quant_rows_kernel<<<grid, 256, 0, stream>>>(x16, rows, cols, ldx, q, ldq, scale_tiles, kcs);
-        else
-            fp4_quant_rows_kernel<<<grid, 256, 0, stream>>>(x32, rows, cols, ldx, q, ldq, scale_tiles, kcs);
+    const bool full = rows % (transpose_out ? kQ4Rows : 128) == 0 && cols % (transpose_out ? kQ4Cols : 128) == 0;
+    auto launch = [&](auto kernel, auto* p, auto... more) {
+        kernel<<<(unsigned)tiles, 256, 0, stream>>>(p, rows, cols, ldx, q, ldq, scale_tiles, (int)kcs, more...);
+    };
+    const int tc = (int)tiles_c;
+    if (xt == FP8BS_BF16) {
+        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(x);
+        if (!transpose_out && full) launch(fp4_quant_rows_kernel<__nv_bfloat16, true>, p);
+        else if (!transpose_out) launch(fp4_quant_rows_kernel<__nv_bfloat16, false>, p);
+        else if (full) launch(fp4_quant_cols_kernel<__nv_bfloat16, true>, p, tc);
+        else launch(fp4_quant_cols_kernel<__nv_bfloat16, false>, p, tc);
     } else {
-        if (xt == FP8BS_BF16)
-            fp4_quant_cols_kernel<<<grid, 256, 0, stream>>>(x16, rows, cols, ldx, q, ldq, scale_tiles, kcs, tiles_c);
-        else
-            fp4_quant_cols_kernel<<<grid, 256, 0, stream>>>(x32, rows, cols, ldx, q, ldq, scale_tiles, kcs, tiles_c);
+        const float* p = static_cast<const float*>(x);
+        if (!transpose_out && full) launch(fp4_quant_rows_kernel<float, true>, p);
+        else if (!transpose_out) launch(fp4_quant_rows_kernel<float, false>, p);
+        else if (full) launch(fp4_quant_cols_kernel<float, true>, p, tc);
+        else launch(fp4_quant_cols_kernel<float, false>, p, tc);
     }
     return launch_status();
 }
@@ -535,12 +539,19 @@ fp8bs_status fp4_dequant_1x32(const uint8_t* q, int64_t ldq, const uint8_t* scal
     const int64_t tiles = cdiv(rows, 128) * cdiv(cols, 128);
     if (tiles > INT32_MAX) return FP8BS_ERR_INVALID_ARG;
     const unsigned grid = (unsigned)tiles;
-    if (ot == FP8BS_BF16)
-        fp4_dequant_kernel<<<grid, 256, 0, stream>>>(q, ldq, scale_tiles, rows, cols, cdiv(cols, 128),
-                                                     static_cast<__nv_bfloat16*>(out), ldo);
-    else
-        fp4_dequant_kernel<<<grid, 256, 0, stream>>>(q, ldq, scale_tiles, rows, cols, cdiv(cols, 128),
-                                                     static_cast<float*>(out), ldo);
+    const bool full = rows % 128 == 0 && cols % 128 == 0;
+    auto launch = [&](auto kernel, auto* p) {
+        kernel<<<grid, 256, 0, stream>>>(q, ldq, scale_tiles, rows, cols, (int)cdiv(cols, 128), p, ldo);
+    };
+    if (ot == FP8BS_BF16) {
+        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(out);
+        if (full) launch(fp4_dequant_kernel<__nv_bfloat16, true>, p);
+        else launch(fp4_dequant_kernel<__nv_bfloat16, false>, p);
+    } else {
+        float* p = static_cast<float*>(out);
+        if (full) launch(fp4_dequant_kernel<float, true>, p);
+        else launch(fp4_dequant_kernel<float, false>, p);
+    }
     return launch_status();
 }
 

@@ -39,38 +39,6 @@ struct NormParams {
     int w_f32, pow2;
 };
 
-// Eight values as four fp32 pairs: the arithmetic below is packed (two lanes an
-// instruction), since these kernels in bf16 come close to the issue rate before
-// they reach the memory's.
-struct Eight {
-    float2 v[4];
-};
-
-template <typename T>
-__device__ __forceinline__ Eight eight_of(const Vec8<T>& a)
-{
-    Eight e;
-    if constexpr (sizeof(T) == 2) {
-        const uint32_t w[4] = {a.raw.x, a.raw.y, a.raw.z, a.raw.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e.v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-    } else {
-        e.v[0] = make_float2(a.a.x, a.a.y);
-        e.v[1] = make_float2(a.a.z, a.a.w);
-        e.v[2] = make_float2(a.b.x, a.b.y);
-        e.v[3] = make_float2(a.b.z, a.b.w);
-    }
-    return e;
-}
-
-__device__ __forceinline__ Eight eight_zero()
-{
-    Eight e;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) e.v[i] = make_float2(0.f, 0.f);
-    return e;
-}
-
 // a + b, rounded to T.  bf16: the packed addition rounds the exact sum once; so
 // does rounding the fp32 sum (the sum of two 8-bit significands is exact in fp32,
 // or else next to one of them and far from a tie).
@@ -189,14 +157,6 @@ __device__ __forceinline__ float row_sum(float v)
     return sum_parts(part[threadIdx.y], blockDim.x >> 5);
 }
 
-__device__ __forceinline__ float absmax(const Eight& e)
-{
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(fmaxf(m, fabsf(e.v[i].x)), fabsf(e.v[i].y));
-    return m;
-}
-
 // Largest of VPT values each over the lanes that differ in the bits TOP, TOP / 2,
 // .., 1: while more than one value is left, a step gives half of them away, so
 // that VPT = 4 takes 5 shuffles over 16 lanes instead of 16.  On return a lane
@@ -293,9 +253,7 @@ __device__ __forceinline__ void quantise_store(const NormParams& p, int64_t r, b
             const uint32_t byte = VPT == 1 ? mine : __shfl_sync(0xffffffffu, mine, (lane & 28) + share_lane<VPT, 2>(i));
             const int c = (i * tx + x) * 8;
             if (inside(c)) {
-                const float f[8] = {y[i].v[0].x, y[i].v[0].y, y[i].v[1].x, y[i].v[1].y,
-                                    y[i].v[2].x, y[i].v[2].y, y[i].v[3].x, y[i].v[3].y};
-                *reinterpret_cast<uint32_t*>(q + (c >> 1)) = mx4_pack8(f, mx4_inv_scale(byte));
+                *reinterpret_cast<uint32_t*>(q + (c >> 1)) = mx4_pack8(y[i], mx4_inv_scale(byte));
             }
         }
     }
