@@ -50,18 +50,20 @@ __global__ void __launch_bounds__(256) fp4_quant_rows_kernel(const T* __restrict
     uint8_t* scales = sf + ((int64_t)rb * kcs + kc) * (int64_t)kSfTileBytes + hw * 16;
     // row 16 i + 32 j past r0
     auto row_ok = [&](int i, int j) { return FULL || (col_ok && r0 + 16 * i + 32 * j < rows); };
+    Vec8<T> v[2][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        Vec8<T> v[4];
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (!FULL) v[j].zero();
-            if (row_ok(i, j)) v[j].load(src + (16 * i + 32 * j) * ldx);
+            if (!FULL) v[i][j].zero();
+            if (row_ok(i, j)) v[i][j].load(src + (16 * i + 32 * j) * ldx);
         }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
         uint32_t word[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const Eight e = eight_of(v[j]);
+            const Eight e = eight_of(v[i][j]);
             const uint32_t byte = mx4_scale_byte(group32_absmax(e));
             if (row_ok(i, j)) *reinterpret_cast<uint32_t*>(dst + (16 * i + 32 * j) * ldq) = mx4_pack8(e, mx4_inv_scale(byte));
             word[j] = sf_gather_word(col_ok ? byte : 127u, lane);
