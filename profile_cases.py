@@ -28,6 +28,15 @@ only the named kernel runs R times):
   gemm_pertensor_small 256 x 4096 x 1024 per-tensor scales, bf16 out
   gemm_rowwise_small   256 x 4096 x 1024 rowwise scales, bf16 out
   quant_rows_<n>, quant_tile_<n>   the quantization sweep at n x n bf16 (n = 1024 ... 32768)
+  norm_fp8     RMS norm of 16640 x 8192 bf16 with the residual's addition, 1x128 e4m3 out
+  norm_fp8_plain       the same without a residual
+  norm_fp4     RMS norm with residual, microscaled 4-bit out
+  norm_back    its backward pass with the residual stream's gradient (two launches)
+  norm_fp8_token       RMS norm of one row of 5120 with residual
+  fp4_quant, fp4_quant_t, fp4_dequant   microscaled 4-bit quantization of a 16640 x 8192 bf16 matrix, along
+               its columns, along its rows (transposed), and back
+  fp4_gemm     4-bit product 16640 x 5120 x 8192, bf16 out
+  fp4_gemm_token, fp4_gemm_small   the same weight with one token; 777 x 1000 x 2080
 With --time, each launch is timed with CUDA events and the mean is printed.
 
   python profile_cases.py configs [--reps R] [--graph]
@@ -227,16 +236,64 @@ def _quant_case(name):
     return fn, nbytes, "GB/s"
 
 
+def _norm_fp4_case(name):
+    """The RMS norm, its backward pass, and the 4-bit quantization and product."""
+    M = inputs.LLAMA4_M
+    if name.startswith("norm"):
+        rows, cols = (1, 5120) if name.endswith("token") else (M, 8192)
+        x = inputs.random_matrix(rows, cols, seed=21).cuda()
+        r = inputs.random_matrix(rows, cols, seed=22).cuda()
+        w = (1.0 + 0.1 * inputs.random_matrix(1, cols, seed=23, dtype=torch.float32)[0]).bfloat16().cuda()
+        n = rows * cols
+        if name == "norm_back":
+            _, _, h, rstd, _ = ops.fp8_rmsnorm_quant_1x128(x, w, r)
+            out = torch.empty_like(h), torch.empty(cols, dtype=torch.float32, device="cuda")
+            ws = ops.rmsnorm_backward_workspace(h)
+            fn = lambda: ops.fp8bs_rmsnorm_backward(x, h, w, rstd, dh=r, out=out, workspace=ws)
+            work = n * 8
+        else:
+            bits = 4 if name == "norm_fp4" else 8
+            res = None if name == "norm_fp8_plain" else r
+            call = ops.fp4_rmsnorm_quant_1x32 if bits == 4 else ops.fp8_rmsnorm_quant_1x128
+            out = ops.rmsnorm_quant_buffers(x, residual=res is not None, bits=bits)
+            fn = lambda: call(x, w, res, out=out)
+            work = n * (2 if res is None else 6) + n * bits // 8 + n // 32
+        torch.cuda.synchronize()
+        return fn, work, "GB/s"
+    if name.startswith("fp4_gemm"):
+        m, n, k = {"fp4_gemm": (M, 5120, 8192), "fp4_gemm_token": (1, 5120, 8192),
+                   "fp4_gemm_small": (777, 1000, 2080)}[name]
+        qa, sa = ops.fp4_quant_1x32(inputs.random_matrix(m, k, seed=24).cuda())
+        qb, sb = ops.fp4_quant_1x32(inputs.random_matrix(n, k, seed=25, scale=k ** -0.5).cuda())
+        out = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+        ws = ops.fp4_scaled_gemm_workspace(m, n, k, "cuda")
+        torch.cuda.synchronize()
+        return (lambda: ops.fp4_scaled_gemm(qa, qb, sa, sb, out=out, workspace=ws)), 2.0 * m * n * k, "TFLOP/s"
+    x = inputs.random_matrix(M, 8192, seed=26).cuda()
+    t = name == "fp4_quant_t"
+    q, s = ops.fp4_quant_1x32(x, transpose_out=t)
+    out = torch.empty_like(x)
+    fn = ((lambda: ops.fp4_dequant_1x32(q, s, out=out)) if name == "fp4_dequant"
+          else (lambda: ops.fp4_quant_1x32(x, transpose_out=t, q=q, scale=s)))
+    torch.cuda.synchronize()
+    return fn, x.numel() * 2 + q.numel() + s.numel(), "GB/s"
+
+
+NORM_FP4_CASES = ["norm_fp8", "norm_fp8_plain", "norm_fp4", "norm_back", "norm_fp8_token", "fp4_quant", "fp4_quant_t",
+                  "fp4_dequant", "fp4_gemm", "fp4_gemm_token", "fp4_gemm_small"]
+
 CONFIG_CASES = (["gemm_tiny", "gemm_pertensor_small", "gemm_rowwise_small", "gemm_fwd", "gemm_dgrad", "gemm_dgrad_wt",
                  "gemm_wgrad", "gemm_tensor", "gemm_rowwise", "gemm_longk", "gemm_fwd_then_quant",
                  "gemm_fwd_quant", "gemm_fwd_quant_only", "gemm_longk_mn", "gemm_grouped", "gemm_grouped_ragged",
                  "gemm_longk_1x128", "gemm_fwd_pow2", "gemm_dgrad_wt_pow2", "gemm_wgrad_pow2", "gemm_longk_pow2",
                  "gemm_longk_1x128_pow2", "quant_dual"]
                 + [f"quant_rows_{n}" for n in inputs.QUANT_SWEEP_SIZES]
-                + [f"quant_tile_{n}" for n in inputs.QUANT_SWEEP_SIZES])
+                + [f"quant_tile_{n}" for n in inputs.QUANT_SWEEP_SIZES] + NORM_FP4_CASES)
 
 
 def _case(name):
+    if name in NORM_FP4_CASES:
+        return _norm_fp4_case(name)
     if name in ("gemm_fwd_quant", "gemm_fwd_quant_only", "gemm_fwd_then_quant"):
         return _fused_case(name)
     if name in ("gemm_grouped", "gemm_grouped_ragged"):
