@@ -590,8 +590,9 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) rmsnorm_back_kernel(co
         }
         // two sets of partial sums: a row's warps may be a block apart
         const float dot = ring_row_sum(dot2.x + dot2.y, g.tx, x, y, part[flip]);
-        // dx = rstd (dy w - n mean(g n)) + dh,  mean(g n) = rstd dot / cols
-        const float k = -(rstd * rstd) * rstd * (dot * inv);
+        // dx = rstd (dy w - n mean(g n)) + dh,  mean(g n) = rstd dot / cols (in this order:
+        // the cube of rstd may leave fp32's range where none of these does)
+        const float k = -(rstd * rstd) * (rstd * (dot * inv));
         const float2 k2 = make_float2(k, k);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {

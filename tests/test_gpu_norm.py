@@ -181,6 +181,17 @@ def test_backward(rows, cols, dtype, residual):
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
 
 
+@pytest.mark.parametrize("rows,cols", [(3, 144), (300, 1040), (4, 16400)])
+@pytest.mark.parametrize("power", [50, -50])
+def test_backward_of_large_and_small_rows(rows, cols, power):
+    """rstd is near 2^-50 or 2^50: its square is in fp32's range, its cube is not."""
+    dy, h, w, _, _ = back_inputs(rows, cols, "fp32", rows + 7)
+    h = torch.ldexp(h, torch.tensor(power))
+    rstd = (1.0 / torch.sqrt(h.double().square().mean(1))).float()
+    got = ops.fp8bs_rmsnorm_backward(dy.cuda(), h.cuda(), w.cuda(), rstd.cuda())
+    check_backward(dy, h, w, rstd, None, got)
+
+
 def test_backward_mixed_weight_pitched_in_place():
     rows, cols = 70, 528
     dy, h, w, rstd, dh = back_inputs(rows, cols, "bf16", 5, wdtype="fp32")
