@@ -23,9 +23,9 @@ __device__ __forceinline__ uint32_t sf_gather_word(uint32_t byte, int lane)
 // Largest magnitude over the four lanes that share a group of 32 values.
 __device__ __forceinline__ float group32_absmax(const Eight& e)
 {
-    float m = absmax(e);
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    float m = absmax<true>(e);
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
 
 // --------------------------------------------------------------------------
@@ -111,12 +111,18 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) fp4_quant_cols_ke
         if (!FULL) b.row[i].zero();
         if (ok) b.row[i].load(src);
     }
-    float m[8];
-    b.col_absmax(m);
+    float m[8] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float f[8];
+        b.row[i].get(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m[j] = max_nan(m[j], fabsf(f[j]));
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 8));
-        m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+        m[j] = max_nan(m[j], __shfl_xor_sync(0xffffffffu, m[j], 8));
+        m[j] = max_nan(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {

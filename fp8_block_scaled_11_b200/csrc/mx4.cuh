@@ -5,7 +5,8 @@
 // group (max|v| taken as at least 1e-12), so that no value saturates; the code
 // is v / r rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (ties to the
 // even code), its highest bit the sign.  v / r is exact in fp32 (r is a power of
-// two), so the code has a single rounding.
+// two), so the code has a single rounding.  A group that holds a NaN or an
+// infinity gets the format's NaN scale (255), whatever its codes.
 //
 // Packed matrix (rows x K): row-major, two codes to a byte, the even column in
 // the low half.  Scale tiles: one 512-byte tile per 128 rows x 4 groups (128
@@ -24,17 +25,25 @@ namespace fp8bs {
 
 constexpr uint32_t kSfTileBytes = 512;
 
-// The scale's byte for a group's largest magnitude (finite, >= 0).
-// max|v| = 1.m * 2^e fits 6 r = 1.5 * 2^2 * r: r = 2^(e - 2), or twice that
-// where 1.m > 1.5.  The floor of 1e-12 keeps the byte at 85 or more; the
-// largest finite fp32 gives 253.
-__device__ __forceinline__ uint32_t mx4_scale_byte(float amax)
+// The larger of a and b, NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b)
 {
-    const uint32_t b = __float_as_uint(fmaxf(amax, 1e-12f));
-    return (b >> 23) - 2u + ((b & 0x7FFFFFu) > 0x400000u ? 1u : 0u);
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
-// 1 / r of a scale byte in [1, 253].
+// The scale's byte for a group's largest magnitude (>= 0, or NaN).
+// max|v| = 1.m * 2^e fits 6 r = 1.5 * 2^2 * r: r = 2^(e - 2), or twice that
+// where 1.m > 1.5.  The floor of 1e-12 keeps the byte at 85 or more; the
+// largest finite fp32 gives 253; an infinity or NaN 255.
+__device__ __forceinline__ uint32_t mx4_scale_byte(float amax)
+{
+    const uint32_t b = __float_as_uint(max_nan(amax, 1e-12f));
+    return b >= 0x7F800000u ? 255u : (b >> 23) - 2u + ((b & 0x7FFFFFu) > 0x400000u ? 1u : 0u);
+}
+
+// 1 / r of a scale byte in [1, 253] (255: an infinity, the codes mean nothing).
 __device__ __forceinline__ float mx4_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
 // r of any scale byte: 2^(byte - 127) (byte 0 is subnormal in fp32), 255 is NaN.
@@ -75,11 +84,19 @@ __device__ __forceinline__ Eight eight_zero()
     return e;
 }
 
+// KEEP: NaN where one of the values is, else such a value does not count.
+template <bool KEEP>
+__device__ __forceinline__ float max_of(float a, float b)
+{
+    return KEEP ? max_nan(a, b) : fmaxf(a, b);
+}
+template <bool KEEP>
 __device__ __forceinline__ float absmax(const Eight& e)
 {
-    float m = 0.f;
+    float m = fabsf(e.v[0].x);
+    m = max_of<KEEP>(m, fabsf(e.v[0].y));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(fmaxf(m, fabsf(e.v[i].x)), fabsf(e.v[i].y));
+    for (int i = 1; i < 4; ++i) m = max_of<KEEP>(max_of<KEEP>(m, fabsf(e.v[i].x)), fabsf(e.v[i].y));
     return m;
 }
 

@@ -161,8 +161,8 @@ __device__ __forceinline__ float row_sum(float v)
 // .., 1: while more than one value is left, a step gives half of them away, so
 // that VPT = 4 takes 5 shuffles over 16 lanes instead of 16.  On return a lane
 // holds the maximum of value i whose bits are the lane's bits TOP (the higher
-// bit of i), TOP / 2.
-template <int VPT, int TOP>
+// bit of i), TOP / 2.  KEEP: NaN where one of the values is.
+template <int VPT, int TOP, bool KEEP>
 __device__ __forceinline__ float share_max(const float (&m)[VPT], int lane)
 {
     float a;
@@ -170,19 +170,19 @@ __device__ __forceinline__ float share_max(const float (&m)[VPT], int lane)
     if constexpr (VPT == 4) {
         const bool hi = lane & TOP, lo = lane & (TOP >> 1);
         float a0 = hi ? m[2] : m[0], a1 = hi ? m[3] : m[1];
-        a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[2], TOP));
-        a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, hi ? m[1] : m[3], TOP));
-        a = fmaxf(lo ? a1 : a0, __shfl_xor_sync(0xffffffffu, lo ? a0 : a1, TOP >> 1));
+        a0 = max_of<KEEP>(a0, __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[2], TOP));
+        a1 = max_of<KEEP>(a1, __shfl_xor_sync(0xffffffffu, hi ? m[1] : m[3], TOP));
+        a = max_of<KEEP>(lo ? a1 : a0, __shfl_xor_sync(0xffffffffu, lo ? a0 : a1, TOP >> 1));
         o = TOP >> 2;
     } else if constexpr (VPT == 2) {
         const bool hi = lane & TOP;
-        a = fmaxf(hi ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[1], TOP));
+        a = max_of<KEEP>(hi ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[1], TOP));
         o = TOP >> 1;
     } else {
         a = m[0];
     }
 #pragma unroll
-    for (; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    for (; o >= 1; o >>= 1) a = max_of<KEEP>(a, __shfl_xor_sync(0xffffffffu, a, o));
     return a;
 }
 
@@ -213,9 +213,9 @@ __device__ __forceinline__ void quantise_store(const NormParams& p, int64_t r, b
     const int lane = threadIdx.x + threadIdx.y * blockDim.x & 31;
     float m[VPT];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) m[i] = absmax(y[i]);
+    for (int i = 0; i < VPT; ++i) m[i] = absmax<BITS == 4>(y[i]);
     if constexpr (BITS == 8) {
-        const float top = share_max<VPT, 8>(m, lane);
+        const float top = share_max<VPT, 8, false>(m, lane);
         const float mine = p.pow2 ? scale_rule<true>(top) : scale_rule<false>(top);
         const int mi = share_index<VPT, 8>(lane);
         const int mc = (mi * tx + (x & ~15)) * 8;               // first column of the lane's own group
@@ -237,7 +237,7 @@ __device__ __forceinline__ void quantise_store(const NormParams& p, int64_t r, b
             }
         }
     } else {
-        const float top = share_max<VPT, 2>(m, lane);
+        const float top = share_max<VPT, 2, true>(m, lane);
         const uint32_t mine = mx4_scale_byte(top);
         const int mi = share_index<VPT, 2>(lane);
         // the chunk's word: its four groups' bytes, groups past the last column 127

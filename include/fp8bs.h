@@ -440,7 +440,8 @@ fp8bs_status fp8_scaled_gemm_grouped(int64_t groups, const int64_t* group_rows, 
  * x, residual, weight, h, y, q and the scales 16-byte aligned, rstd 4-byte;
  * leading dims in bytes multiples of 16; ld_scale % 4 == 0.  eps >= 0; eps = 0
  * with an all-zero row divides by zero.  Inputs must be finite, and a row's sum
- * of squares and its y must fit fp32.  Other than h, no output may overlap an
+ * of squares and its y must fit fp32: a row where they are not has a NaN rstd, and
+ * NaN in all its e4m3 codes or 4-bit scales.  Other than h, no output may overlap an
  * input or another output.  Errors as the quantizations.
  */
 fp8bs_status fp8_rmsnorm_quant_1x128(const void* x, int64_t ldx, const void* residual, int64_t ld_res, fp8bs_dtype xt,
@@ -493,6 +494,9 @@ fp8bs_status fp8bs_rmsnorm_backward(const void* dy, int64_t lddy, const void* h,
  *       power-of-two rule of the 8-bit formats with 6 for 448), so that no value
  *       saturates;
  *   code = v / r rounded to nearest, ties to the even code (sign in bit 3, -0 kept).
+ * A group that holds a NaN or an infinity, for which the codes have no value, gets
+ * the format's NaN scale (e = 255): its values are NaN, and so is its row of a
+ * product.
  *
  * transpose_out = 0: groups along the contiguous dim of x.  q: rows x cols/2
  *            bytes, two codes each (the even column in the low four bits),

@@ -93,6 +93,32 @@ def test_quant_every_border():
     assert np.array_equal(ref.unpack(q.cpu().numpy()), code) and np.all(e == 127)
 
 
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,cols", [(256, 256), (160, 96)])
+def test_quant_nan_and_infinity(rows, cols, dtype, transpose):
+    """A group with a NaN or an infinity has the NaN scale and NaN values; every other group is as without them."""
+    x = values(rows, cols, rows, DT[dtype])
+    bad = x.clone()
+    at = [(0, 0, float("nan")), (5, 95, float("inf")), (37, 40, -float("inf")), (rows - 1, cols - 1, -float("nan")),
+          (130, 64, float("inf")), (130, 65, float("nan"))]
+    hit = torch.zeros(rows, cols, dtype=torch.bool)
+    for i, j, v in at:
+        bad[i, j] = v
+        if transpose:
+            hit[i // 32 * 32:i // 32 * 32 + 32, j] = True
+        else:
+            hit[i, j // 32 * 32:j // 32 * 32 + 32] = True
+    q, s = ops.fp4_quant_1x32(x.cuda(), transpose_out=transpose)
+    qb, sb = ops.fp4_quant_1x32(bad.cuda(), transpose_out=transpose)
+    v, vb = (ops.fp4_dequant_1x32(*t, out_dtype=torch.float32).cpu() for t in ((q, s), (qb, sb)))
+    hit = hit.t() if transpose else hit
+    assert torch.equal(torch.isnan(vb), hit) and torch.equal(v[~hit], vb[~hit])
+    R, C = hit.shape
+    e = sb.cpu().numpy().reshape(-1)[ref.tile_index(R, C // 32)]
+    assert np.array_equal(e == 255, hit.reshape(R, C // 32, 32).any(2).numpy())
+
+
 def test_quant_strides_and_guards():
     """Views with pitches: nothing outside the matrix is written, and scale bytes past the last row stay."""
     rows, cols = 130, 96
@@ -264,3 +290,27 @@ def test_product_deterministic_and_captured():
     side.synchronize()
     assert torch.equal(first, out)
     no_device_error()
+
+
+def test_past_32_bit_offsets():
+    """More than 2^31 elements: the last rows equal the same rows on their own; the last columns too."""
+    rows, cols, tail = 131200, 16384, 256
+    x = torch.randn(rows, cols, device="cuda", dtype=torch.bfloat16, generator=torch.Generator(device="cuda").manual_seed(2))
+    q, s = ops.fp4_quant_1x32(x)
+    q1, s1 = ops.fp4_quant_1x32(x[-tail:])
+    assert torch.equal(q[-tail:], q1) and torch.equal(s[-tail // 128:], s1)
+    v = ops.fp4_dequant_1x32(q, s)
+    assert torch.equal(v[-tail:], ops.fp4_dequant_1x32(q1, s1))
+    del v
+    qt, st = ops.fp4_quant_1x32(x, transpose_out=True)
+    qt1, st1 = ops.fp4_quant_1x32(x[:, -128:], transpose_out=True)
+    assert torch.equal(qt[-128:], qt1) and torch.equal(st[-1:], st1)
+    # D of 70016 x 32000 bf16; codes of small integers and scales of one: every sum is exact in any order
+    M, N, K = 70016, 32000, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    a, b = (torch.randint(0, 256, (n, K // 2), device="cuda", dtype=torch.uint8, generator=g) for n in (M, N))
+    sa, sb = (torch.full_like(ops.fp4_scale_tiles(n, K, "cuda"), 127) for n in (M, N))
+    d = ops.fp4_scaled_gemm(a, b, sa, sb)
+    d1 = ops.fp4_scaled_gemm(a[-tail:], b, sa[-tail // 128:].contiguous(), sb)
+    no_device_error()
+    assert torch.equal(d[-tail:], d1)

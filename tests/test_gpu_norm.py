@@ -121,6 +121,25 @@ def test_forward_zero_rows():
     assert bool((q[0] == 0).all()) and bool((q[1] != 0).all())
 
 
+@pytest.mark.parametrize("rows,cols", [(3, 512), (300, 8192), (310, 2080), (2, 16640)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 1e25])
+def test_forward_row_out_of_range(rows, cols, value):
+    """A NaN, an infinity or a sum of squares past fp32 makes its row NaN in either format, and no other row."""
+    x, r, w = make(rows, cols, "bf16", 11)
+    bad = x.clone()
+    bad[1, 37] = value
+    keep = [i for i in range(rows) if i != 1]
+    for bits, fn in ((8, ops.fp8_rmsnorm_quant_1x128), (4, ops.fp4_rmsnorm_quant_1x32)):
+        q, s, _, rstd, _ = fn(x.cuda(), w.cuda(), r.cuda(), eps=EPS)
+        qb, sb, _, rb, _ = fn(bad.cuda(), w.cuda(), r.cuda(), eps=EPS)
+        assert torch.equal(q[keep], qb[keep]) and torch.equal(rstd[keep], rb[keep]) and bool(torch.isnan(rb[1]))
+        if bits == 8:
+            assert bool(torch.isnan(qb.view(torch.float8_e4m3fn).float()[1]).all())
+        else:
+            assert bool(torch.isnan(ops.fp4_dequant_1x32(qb, sb)[1]).all())
+            assert torch.equal(ops.fp4_dequant_1x32(q, s)[keep], ops.fp4_dequant_1x32(qb, sb)[keep])
+
+
 @pytest.mark.parametrize("rows,cols", [(3, 512), (300, 1024), (2, 16640)])
 def test_forward_in_place_and_pitched(rows, cols):
     """h over the residual, and over x; pitched views; nothing else is written."""
@@ -261,6 +280,24 @@ def test_norm_then_product_8_and_4_bits():
     check_backward(dy.cpu(), h.cpu(), w, rstd.cpu(), r, (dx, dw))
     st = ops.fp8bs_check_device_error()
     assert st == 0, ops.fp8bs_status_string(st)
+
+
+def test_past_32_bit_offsets():
+    """More than 2^31 elements: the last rows equal the same rows on their own (each row's result is its own)."""
+    rows, cols, tail = 131200, 16384, 512
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(rows, cols, device="cuda", dtype=torch.bfloat16, generator=g)
+    r = torch.randn(rows, cols, device="cuda", dtype=torch.bfloat16, generator=g)
+    w = torch.randn(cols, device="cuda", generator=g).bfloat16()
+    last = slice(rows - tail, rows)
+    for fn in (ops.fp8_rmsnorm_quant_1x128, ops.fp4_rmsnorm_quant_1x32):
+        q, s, h, rstd, _ = fn(x, w, r)
+        q1, s1, h1, rstd1, _ = fn(x[last], w, r[last])
+        assert torch.equal(q[last], q1) and torch.equal(h[last], h1) and torch.equal(rstd[last], rstd1)
+        assert torch.equal(s[last] if s.dim() == 2 else s[-(tail // 128):], s1)
+    dx, _ = ops.fp8bs_rmsnorm_backward(x, h, w, rstd, dh=r)
+    dx1, _ = ops.fp8bs_rmsnorm_backward(x[last], h1, w, rstd1, dh=r[last])
+    assert torch.equal(dx[last], dx1)
 
 
 def test_captured_with_eager_alive():
