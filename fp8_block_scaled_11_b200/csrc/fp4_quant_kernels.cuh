@@ -20,18 +20,54 @@ __device__ __forceinline__ uint32_t sf_gather_word(uint32_t byte, int lane)
     return w | __shfl_xor_sync(0xffffffffu, w, 8);
 }
 
-// Largest magnitude over the four lanes that share a group of 32 values.
-__device__ __forceinline__ float group32_absmax(const Eight& e)
+// Largest of VPT values each over the lanes that differ in the bits TOP, TOP / 2,
+// .., 1: while more than one value is left, a step gives half of them away, so
+// that VPT = 4 takes 5 shuffles over 16 lanes instead of 16.  On return a lane
+// holds the maximum of value i whose bits are the lane's bits TOP (the higher
+// bit of i), TOP / 2.  KEEP: NaN where one of the values is.
+template <int VPT, int TOP, bool KEEP>
+__device__ __forceinline__ float share_max(const float (&m)[VPT], int lane)
 {
-    float m = absmax<true>(e);
-    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    return max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    float a;
+    int o = TOP;
+    if constexpr (VPT == 4) {
+        const bool hi = lane & TOP, lo = lane & (TOP >> 1);
+        float a0 = hi ? m[2] : m[0], a1 = hi ? m[3] : m[1];
+        a0 = max_of<KEEP>(a0, __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[2], TOP));
+        a1 = max_of<KEEP>(a1, __shfl_xor_sync(0xffffffffu, hi ? m[1] : m[3], TOP));
+        a = max_of<KEEP>(lo ? a1 : a0, __shfl_xor_sync(0xffffffffu, lo ? a0 : a1, TOP >> 1));
+        o = TOP >> 2;
+    } else if constexpr (VPT == 2) {
+        const bool hi = lane & TOP;
+        a = max_of<KEEP>(hi ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[1], TOP));
+        o = TOP >> 1;
+    } else {
+        a = m[0];
+    }
+#pragma unroll
+    for (; o >= 1; o >>= 1) a = max_of<KEEP>(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return a;
+}
+
+// The value index a lane holds after share_max, and the lane (of its TOP * 2
+// lanes) that holds value i.
+template <int VPT, int TOP>
+__device__ __forceinline__ int share_index(int lane)
+{
+    if (VPT == 4) return ((lane & TOP) ? 2 : 0) + ((lane & (TOP >> 1)) ? 1 : 0);
+    return VPT == 2 && (lane & TOP) ? 1 : 0;
+}
+template <int VPT, int TOP>
+__device__ __forceinline__ int share_lane(int i)
+{
+    if (VPT == 4) return (i >> 1) * TOP + (i & 1) * (TOP >> 1);
+    return VPT == 2 ? i * TOP : 0;
 }
 
 // --------------------------------------------------------------------------
 // Groups along the columns.  A CTA owns a scale tile's 128 rows x 128 columns;
 // half-warp h of 16 takes rows h, h + 16 (mod 32) of each of the four 32-row
-// quarters, whose scale words are adjacent in the tile (one 16-byte store).
+// quarters, whose scale words are adjacent in the tile (16 bytes of one store).
 // FULL: rows and columns are multiples of 128, nothing is tested.
 // --------------------------------------------------------------------------
 template <typename T, bool FULL>
@@ -60,24 +96,25 @@ __global__ void __launch_bounds__(256) fp4_quant_rows_kernel(const T* __restrict
         }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        uint32_t word[4];
+        // lane l of a group's four takes row l's maximum: one scale a lane
+        Eight e[4];
+        float m[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const Eight e = eight_of(v[i][j]);
-            const uint32_t byte = mx4_scale_byte(group32_absmax(e));
-            if (row_ok(i, j)) *reinterpret_cast<uint32_t*>(dst + (16 * i + 32 * j) * ldq) = mx4_pack8(e, mx4_inv_scale(byte));
-            word[j] = sf_gather_word(col_ok ? byte : 127u, lane);
+            e[j] = eight_of(v[i][j]);
+            m[j] = absmax<true>(e[j]);
+        }
+        const uint32_t mine = mx4_scale_byte(share_max<4, 2, true>(m, lane));
+        const uint32_t word = sf_gather_word(col_ok ? mine : 127u, lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t byte = __shfl_sync(0xffffffffu, mine, (lane & 28) + share_lane<4, 2>(j));
+            if (row_ok(i, j)) *reinterpret_cast<uint32_t*>(dst + (16 * i + 32 * j) * ldq) = mx4_pack8(e[j], mx4_inv_scale(byte));
         }
         // rows past the last one keep their bytes
-        if ((lane & 15) == 0) {
-            if (FULL || r0 + 16 * i + 96 < rows) {
-                *reinterpret_cast<uint4*>(scales + 256 * i) = make_uint4(word[0], word[1], word[2], word[3]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (r0 + 16 * i + 32 * j < rows) *reinterpret_cast<uint32_t*>(scales + 256 * i + 4 * j) = word[j];
-            }
-        }
+        const int own = share_index<4, 2>(lane);
+        if ((lane & 12) == 0 && (FULL || r0 + 16 * i + 32 * own < rows))
+            *reinterpret_cast<uint32_t*>(scales + 256 * i + 4 * own) = word;
     }
 }
 
@@ -91,6 +128,51 @@ __global__ void __launch_bounds__(256) fp4_quant_rows_kernel(const T* __restrict
 // FULL: whole tiles only, nothing is tested.
 // --------------------------------------------------------------------------
 constexpr int kQ4Rows = 256, kQ4Cols = 64;
+
+// The scale bytes of a group's eight columns, whose 32 rows are in the four
+// lanes that differ in bits 3 and 4.  bf16: the magnitudes are compared as
+// unsigned 16-bit halves (in the order of the values, NaN above infinity), two
+// columns a word; half the words are given away at each step, so that a lane
+// ends with one word and two scales, which it hands back.
+__device__ __forceinline__ void col_scale_bytes(const Block8x8<__nv_bfloat16>& b, uint32_t (&byte)[8], int lane)
+{
+    uint32_t m[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        m[0] = __vmaxu2(m[0], b.row[i].raw.x & 0x7FFF7FFFu);
+        m[1] = __vmaxu2(m[1], b.row[i].raw.y & 0x7FFF7FFFu);
+        m[2] = __vmaxu2(m[2], b.row[i].raw.z & 0x7FFF7FFFu);
+        m[3] = __vmaxu2(m[3], b.row[i].raw.w & 0x7FFF7FFFu);
+    }
+    const bool hi = lane & 16, lo = lane & 8;
+    const uint32_t a0 = __vmaxu2(hi ? m[2] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[2], 16));
+    const uint32_t a1 = __vmaxu2(hi ? m[3] : m[1], __shfl_xor_sync(0xffffffffu, hi ? m[1] : m[3], 16));
+    const uint32_t a = __vmaxu2(lo ? a1 : a0, __shfl_xor_sync(0xffffffffu, lo ? a0 : a1, 8));
+    const uint32_t mine = mx4_scale_byte(__uint_as_float(a << 16)) | mx4_scale_byte(__uint_as_float(a & 0xFFFF0000u)) << 16;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t two = __shfl_sync(0xffffffffu, mine, (lane & 7) + (j >> 1) * 16 + (j & 1) * 8);
+        byte[2 * j] = two & 0xFFFFu;
+        byte[2 * j + 1] = two >> 16;
+    }
+}
+__device__ __forceinline__ void col_scale_bytes(const Block8x8<float>& b, uint32_t (&byte)[8], int)
+{
+    float m[8] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float f[8];
+        b.row[i].get(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m[j] = max_nan(m[j], fabsf(f[j]));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        m[j] = max_nan(m[j], __shfl_xor_sync(0xffffffffu, m[j], 8));
+        m[j] = max_nan(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+        byte[j] = mx4_scale_byte(m[j]);
+    }
+}
 
 template <typename T, bool FULL>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) fp4_quant_cols_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
@@ -111,22 +193,11 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) fp4_quant_cols_ke
         if (!FULL) b.row[i].zero();
         if (ok) b.row[i].load(src);
     }
-    float m[8] = {};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float f[8];
-        b.row[i].get(f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = max_nan(m[j], fabsf(f[j]));
-    }
+    uint32_t bytes[8];
+    col_scale_bytes(b, bytes, threadIdx.x & 31);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        m[j] = max_nan(m[j], __shfl_xor_sync(0xffffffffu, m[j], 8));
-        m[j] = max_nan(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t byte = mx4_scale_byte(m[j]);
+        const uint32_t byte = bytes[j];
         Eight e;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

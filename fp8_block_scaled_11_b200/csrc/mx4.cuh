@@ -35,12 +35,12 @@ __device__ __forceinline__ float max_nan(float a, float b)
 
 // The scale's byte for a group's largest magnitude (>= 0, or NaN).
 // max|v| = 1.m * 2^e fits 6 r = 1.5 * 2^2 * r: r = 2^(e - 2), or twice that
-// where 1.m > 1.5.  The floor of 1e-12 keeps the byte at 85 or more; the
+// where 1.m > 1.5 (the addition carries into the exponent then).  The floor of 1e-12 keeps the byte at 85 or more; the
 // largest finite fp32 gives 253; an infinity or NaN 255.
 __device__ __forceinline__ uint32_t mx4_scale_byte(float amax)
 {
     const uint32_t b = __float_as_uint(max_nan(amax, 1e-12f));
-    return b >= 0x7F800000u ? 255u : (b >> 23) - 2u + ((b & 0x7FFFFFu) > 0x400000u ? 1u : 0u);
+    return b >= 0x7F800000u ? 255u : ((b + 0x3FFFFFu) >> 23) - 2u;
 }
 
 // 1 / r of a scale byte in [1, 253] (255: an infinity, the codes mean nothing).

@@ -157,50 +157,6 @@ __device__ __forceinline__ float row_sum(float v)
     return sum_parts(part[threadIdx.y], blockDim.x >> 5);
 }
 
-// Largest of VPT values each over the lanes that differ in the bits TOP, TOP / 2,
-// .., 1: while more than one value is left, a step gives half of them away, so
-// that VPT = 4 takes 5 shuffles over 16 lanes instead of 16.  On return a lane
-// holds the maximum of value i whose bits are the lane's bits TOP (the higher
-// bit of i), TOP / 2.  KEEP: NaN where one of the values is.
-template <int VPT, int TOP, bool KEEP>
-__device__ __forceinline__ float share_max(const float (&m)[VPT], int lane)
-{
-    float a;
-    int o = TOP;
-    if constexpr (VPT == 4) {
-        const bool hi = lane & TOP, lo = lane & (TOP >> 1);
-        float a0 = hi ? m[2] : m[0], a1 = hi ? m[3] : m[1];
-        a0 = max_of<KEEP>(a0, __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[2], TOP));
-        a1 = max_of<KEEP>(a1, __shfl_xor_sync(0xffffffffu, hi ? m[1] : m[3], TOP));
-        a = max_of<KEEP>(lo ? a1 : a0, __shfl_xor_sync(0xffffffffu, lo ? a0 : a1, TOP >> 1));
-        o = TOP >> 2;
-    } else if constexpr (VPT == 2) {
-        const bool hi = lane & TOP;
-        a = max_of<KEEP>(hi ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[1], TOP));
-        o = TOP >> 1;
-    } else {
-        a = m[0];
-    }
-#pragma unroll
-    for (; o >= 1; o >>= 1) a = max_of<KEEP>(a, __shfl_xor_sync(0xffffffffu, a, o));
-    return a;
-}
-
-// The value index a lane holds after share_max, and the lane (of its TOP * 2
-// lanes) that holds value i.
-template <int VPT, int TOP>
-__device__ __forceinline__ int share_index(int lane)
-{
-    if (VPT == 4) return ((lane & TOP) ? 2 : 0) + ((lane & (TOP >> 1)) ? 1 : 0);
-    return VPT == 2 && (lane & TOP) ? 1 : 0;
-}
-template <int VPT, int TOP>
-__device__ __forceinline__ int share_lane(int i)
-{
-    if (VPT == 4) return (i >> 1) * TOP + (i & 1) * (TOP >> 1);
-    return VPT == 2 ? i * TOP : 0;
-}
-
 // VPT eights of normalised values of row r, columns (i tx + x) 8 .. + 7 (zero past
 // the last column): quantised and stored with their groups' scales.  Whole warps
 // take part; 16 neighbouring lanes (4 for the groups of 32) hold a group.
