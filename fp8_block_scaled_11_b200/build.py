@@ -1,11 +1,15 @@
-"""Build step for the CUDA library: csrc/fp8bs_lib.cu -> libfp8bs.so (in-tree).
+"""Build step, in-tree: the CUDA library (csrc/fp8bs_lib.cu -> libfp8bs.so) and
+the extension module over it that ops.py calls for the norm and the 4-bit
+operators (csrc/binding.cpp -> _binding.so).
 
-Compiled for sm_100a only (B200), no fast-math: the quantization's fp32
-division and reciprocal must be IEEE round-to-nearest.
+The library is compiled for sm_100a only (B200), no fast-math: the
+quantization's fp32 division and reciprocal must be IEEE round-to-nearest.
 """
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -13,6 +17,8 @@ SRC_DIR = os.path.join(HERE, "csrc")
 MAIN = os.path.join(SRC_DIR, "fp8bs_lib.cu")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(HERE, "libfp8bs.so")
+BINDING = os.path.join(SRC_DIR, "binding.cpp")
+BINDING_PATH = os.path.join(HERE, "_binding.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -30,23 +36,42 @@ def _sources():
     return out
 
 
-def needs_build() -> bool:
-    if not os.path.exists(LIB_PATH):
+def _older(path: str, sources) -> bool:
+    if not os.path.exists(path):
         return True
-    t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(s) > t for s in _sources())
+    t = os.path.getmtime(path)
+    return any(os.path.getmtime(s) > t for s in sources)
+
+
+def needs_build() -> bool:
+    return _older(LIB_PATH, _sources())
+
+
+def _run(cmd, path: str):
+    """Runs cmd with a temporary output, which then takes path's place."""
+    tmp = path + f".tmp{os.getpid()}"
+    subprocess.run([*cmd, "-o", tmp], check=True)
+    os.replace(tmp, path)
+
+
+def _build_binding():
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
+          "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"),
+          "-isystem", os.path.join(cuda, "include"), BINDING, "-L", HERE, "-l:libfp8bs.so",
+          "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+          "-Wl,-rpath,$ORIGIN"], BINDING_PATH)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not needs_build():
-        return LIB_PATH
-    nvcc = os.environ.get("NVCC", "nvcc")
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc, *NVCC_FLAGS, "-I", INCLUDE, MAIN, "-o", tmp]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB_PATH)
+    if force or needs_build():
+        cmd = [os.environ.get("NVCC", "nvcc"), *NVCC_FLAGS, "-I", INCLUDE, MAIN]
+        if verbose:
+            cmd.insert(1, "-Xptxas=-v")
+        _run(cmd, LIB_PATH)
+    if force or _older(BINDING_PATH, [BINDING, os.path.join(INCLUDE, "fp8bs.h")]):
+        _build_binding()
     return LIB_PATH
 
 

@@ -401,70 +401,18 @@ def fp8_scaled_gemm_quant(A: torch.Tensor, Bt: torch.Tensor, scale_a: torch.Tens
 
 
 # ---------------------------------------------------------------------------- norm and 4-bit helpers
-# These calls are short on the GPU (a few microseconds for a token), so their
-# checks are written to cost little: one comparison per property.
-def _mat(t: torch.Tensor, shape, dtype, dev, what: str):
-    """Address and leading dimension of a row-major matrix of this shape, dtype and device."""
-    if t.shape != shape or t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{what}: expected {tuple(shape)} {dtype} on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
-    ld, one = t.stride()
-    if one != 1:
-        raise ValueError(f"{what}: expected a row-major matrix (unit column stride)")
-    return t.data_ptr(), ld if shape[0] != 1 else shape[1]      # one row: any stride will do
+_native = None
 
 
-def _vec(t: torch.Tensor, n: int, dev, what: str) -> int:
-    """Address of a contiguous vector of n elements on this device."""
-    if t.dim() != 1 or t.numel() != n or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous vector of {n} elements on {dev}, got {tuple(t.shape)} on "
-                         f"{t.device}")
-    return t.data_ptr()
-
-
-def _vec32(t: torch.Tensor, n: int, dev, what: str) -> int:
-    if t.dtype != torch.float32:
-        raise ValueError(f"{what}: expected fp32, got {t.dtype}")
-    return _vec(t, n, dev, what)
-
-
-def _buffer(t: Optional[torch.Tensor], dev, what: str):
-    """Address and bytes of a scratch buffer (0, 0 for none)."""
-    if t is None:
-        return 0, 0
-    if t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous buffer on {dev}")
-    return t.data_ptr(), t.numel() * t.element_size()
-
-
-def _tiles(s: torch.Tensor, rows: int, cols: int, dev, what: str) -> int:
-    if (s.dtype != torch.uint8 or s.device != dev or not s.is_contiguous()
-            or s.numel() != (rows + 127) // 128 * ((cols + 127) // 128) * 512):
-        raise ValueError(f"{what}: expected the fp4_scale_tiles of a {rows} x {cols} matrix on {dev}")
-    return s.data_ptr()
-
-
-_DTYPE_CODES = {torch.bfloat16: BF16, torch.float32: F32}
-
-
-def _code(t: torch.Tensor, what: str) -> int:
-    c = _DTYPE_CODES.get(t.dtype)
-    if c is None:
-        raise TypeError(f"{what}: unsupported dtype {t.dtype} (bf16 or fp32)")
-    return c
-
-
-def _call(fn: str, dev: torch.device, *args):
-    """Calls the C entry point on dev's current stream, with dev current."""
-    index = dev.index
-    if index is None:
-        raise ValueError(f"{fn}: expected CUDA tensors, got {dev}")
-    if index != torch._C._cuda_getDevice():
-        with torch.cuda.device(index):
-            status = getattr(_lib or lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        status = getattr(_lib or lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(index))
-    if status != FP8BS_OK:
-        raise Fp8bsError(fn, status)
+def _load_native():
+    """The extension module that checks the arguments of the functions below and calls the library (csrc/binding.cpp)."""
+    global _native
+    lib()
+    if not os.path.exists(_build.BINDING_PATH):
+        raise ImportError(f"_binding.so not built ({_build.BINDING_PATH}); run fp8_block_scaled_11_b200/build.py")
+    from . import _binding
+    _native = _binding
+    return _native
 
 
 # ---------------------------------------------------------------------------- microscaled 4 bits
@@ -480,53 +428,38 @@ def _packed(rows: int, cols: int, device) -> torch.Tensor:
     return torch.empty((rows, _round_up(cols // 2, 16)), dtype=torch.uint8, device=device)[:, :cols // 2]
 
 
-def _codes(q: torch.Tensor, what: str):
-    """rows, codes per row, address and leading dimension (bytes) of packed codes."""
-    if q.dtype != torch.uint8:
-        raise TypeError(f"{what}: packed 4-bit codes are uint8")
-    rows, half = q.shape
-    ld, one = q.stride()
-    if one != 1:
-        raise ValueError(f"{what}: expected a row-major matrix (unit column stride)")
-    return rows, 2 * half, q.data_ptr(), ld if rows != 1 else half
-
-
 def fp4_quant_1x32(x: torch.Tensor, transpose_out: bool = False, q: Optional[torch.Tensor] = None,
                    scale: Optional[torch.Tensor] = None):
     """Microscaled 4-bit quantization: returns (q uint8 rows x cols/2, scale
     tiles).  transpose_out=False: groups of 32 along the columns of x (cols %
     32 == 0).  transpose_out=True: groups along its rows (rows % 32 == 0); q is
     cols x rows/2.  Preallocated outputs may be passed as q / scale."""
-    rows, cols = x.shape
-    dev, xt = x.device, _code(x, "x")
-    xp, ldx = _mat(x, x.shape, x.dtype, dev, "x")
-    R, C = (cols, rows) if transpose_out else (rows, cols)
-    if q is None:
-        q = _packed(R, C, dev)
-    if scale is None:
-        scale = fp4_scale_tiles(R, C, dev)
-    qp, ldq = _mat(q, (R, C // 2), torch.uint8, dev, "q")
-    _call("fp4_quant_1x32", dev, xp, xt, rows, cols, ldx, qp, ldq, _tiles(scale, R, C, dev, "scale"),
-          int(transpose_out))
+    if q is None or scale is None:
+        rows, cols = x.shape
+        if transpose_out:
+            rows, cols = cols, rows
+        q = _packed(rows, cols, x.device) if q is None else q
+        scale = fp4_scale_tiles(rows, cols, x.device) if scale is None else scale
+    status = (_native or _load_native()).quant(x, transpose_out, q, scale)
+    if status:
+        raise Fp8bsError("fp4_quant_1x32", status)
     return q, scale
 
 
 def fp4_dequant_1x32(q: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16,
                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of packed 4-bit codes and their scale tiles."""
-    rows, cols, qp, ldq = _codes(q, "q")
-    dev = q.device
     if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
-    op, ldo = _mat(out, (rows, cols), out.dtype, dev, "out")
-    _call("fp4_dequant_1x32", dev, qp, ldq, _tiles(scale, rows, cols, dev, "scale"), rows, cols, op,
-          _code(out, "out"), ldo)
+        out = torch.empty((q.shape[0], 2 * q.shape[1]), dtype=out_dtype, device=q.device)
+    status = (_native or _load_native()).dequant(q, scale, out)
+    if status:
+        raise Fp8bsError("fp4_dequant_1x32", status)
     return out
 
 
 def fp4_scaled_gemm_workspace(M: int, N: int, K: int, device) -> Optional[torch.Tensor]:
     """Allocate the split-K workspace of a product of these sizes (None where it needs none)."""
-    n = int(lib().fp4_scaled_gemm_workspace_size(M, N, K))
+    n = (_native or _load_native()).product_workspace(M, N, K)
     return torch.empty((n,), dtype=torch.uint8, device=device) if n else None
 
 
@@ -536,20 +469,16 @@ def fp4_scaled_gemm(A: torch.Tensor, Bt: torch.Tensor, scale_a: torch.Tensor, sc
     """D = A . Bt^T of two microscaled 4-bit matrices: A M x K/2 and Bt N x K/2
     uint8 (two codes a byte) with their scale tiles, as fp4_quant_1x32 returns
     them.  D: M x N, bf16 or fp32."""
-    M, K, ap, lda = _codes(A, "A")
-    N, K2, bp, ldb = _codes(Bt, "Bt")
-    dev = A.device
-    if K2 != K or Bt.device != dev:
-        raise ValueError("A and Bt must share K and the device")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-    dp, ldd = _mat(out, (M, N), out.dtype, dev, "out")
-    oc = _code(out, "out")
-    if split_k and workspace is None:
-        workspace = fp4_scaled_gemm_workspace(M, N, K, dev)
-    wp, wn = _buffer(workspace if split_k else None, dev, "workspace")
-    _call("fp4_scaled_gemm", dev, M, N, K, ap, lda, bp, ldb, _tiles(scale_a, M, K, dev, "scale_a"),
-          _tiles(scale_b, N, K, dev, "scale_b"), dp, ldd, oc, wp, wn)
+        out = torch.empty((A.shape[0], Bt.shape[0]), dtype=out_dtype, device=A.device)
+    if not split_k:
+        workspace = None
+    elif workspace is None:
+        M, half = A.shape
+        workspace = fp4_scaled_gemm_workspace(M, Bt.shape[0], 2 * half, A.device)
+    status = (_native or _load_native()).product(A, Bt, scale_a, scale_b, out, workspace)
+    if status:
+        raise Fp8bsError("fp4_scaled_gemm", status)
     return out
 
 
@@ -572,23 +501,6 @@ def rmsnorm_quant_buffers(x: torch.Tensor, residual: bool = False, want_y: bool 
             torch.empty((rows, cols), dtype=x.dtype, device=dev) if want_y else None)
 
 
-def _norm_args(x, weight, residual, out, eps, bits):
-    """The arguments both forward entry points share, from x to the leading dimension of q."""
-    shape, dt, dev = x.shape, x.dtype, x.device
-    rows, cols = shape
-    q, _, h, rstd, y = out
-    xt = _code(x, "x")
-    xp, ldx = _mat(x, shape, dt, dev, "x")
-    if (h is None) != (residual is None):
-        raise ValueError("out has h exactly where there is a residual")
-    rp, ldr = (0, 0) if residual is None else _mat(residual, shape, dt, dev, "residual")
-    hp, ldh = (0, 0) if h is None else _mat(h, shape, dt, dev, "h")
-    yp, ldy = (0, 0) if y is None else _mat(y, shape, dt, dev, "y")
-    qp, ldq = _mat(q, (rows, cols * bits // 8), torch.uint8, dev, "q")
-    return (xp, ldx, rp, ldr, xt, rows, cols, _vec(weight, cols, dev, "weight"), _code(weight, "weight"), eps, hp, ldh,
-            _vec32(rstd, rows, dev, "rstd"), yp, ldy, qp, ldq)
-
-
 def fp8_rmsnorm_quant_1x128(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
                             eps: float = 1e-6, want_y: bool = False, out=None, rule: int = SCALE_RULE_FP32):
     """RMS norm of h = x + residual with its result quantized 1x128 in e4m3:
@@ -597,15 +509,10 @@ def fp8_rmsnorm_quant_1x128(x: torch.Tensor, weight: torch.Tensor, residual: Opt
     passed as out (rmsnorm_quant_buffers); h may be x or residual itself."""
     if out is None:
         out = rmsnorm_quant_buffers(x, residual is not None, want_y)
-    args = _norm_args(x, weight, residual, out, eps, 8)
     q, s, h, rstd, y = out
-    rows, cols = x.shape
-    if s.shape != (rows, (cols + 127) // 128) or s.device != x.device:
-        raise ValueError(f"scale_inv: expected a ({rows}, {(cols + 127) // 128}) grid on {x.device}")
-    one, ld = s.stride()
-    if one != 1 or s.dtype != torch.float32 or ld < rows:
-        ld = _grid_ld(s, rows)
-    _call("fp8_rmsnorm_quant_1x128", x.device, *args, s.data_ptr(), ld, rule)
+    status = (_native or _load_native()).norm(8, rule, x, weight, residual, eps, q, s, h, rstd, y)
+    if status:
+        raise Fp8bsError("fp8_rmsnorm_quant_1x128", status)
     return q, s, x if residual is None else h, rstd, y
 
 
@@ -615,9 +522,10 @@ def fp4_rmsnorm_quant_1x32(x: torch.Tensor, weight: torch.Tensor, residual: Opti
     cols/2 packed codes, the scales are scale tiles (bits=4 buffers)."""
     if out is None:
         out = rmsnorm_quant_buffers(x, residual is not None, want_y, 4)
-    args = _norm_args(x, weight, residual, out, eps, 4)
     q, s, h, rstd, y = out
-    _call("fp4_rmsnorm_quant_1x32", x.device, *args, _tiles(s, x.shape[0], x.shape[1], x.device, "scale"))
+    status = (_native or _load_native()).norm(4, 0, x, weight, residual, eps, q, s, h, rstd, y)
+    if status:
+        raise Fp8bsError("fp4_rmsnorm_quant_1x32", status)
     return q, s, x if residual is None else h, rstd, y
 
 
@@ -633,20 +541,13 @@ def fp8bs_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     y), the forward pass's h and rstd, and dh (the gradient that reaches h past
     the norm; added to dx).  Preallocated outputs may be passed as out=(dx,
     dweight); dx may be dy, dh or h itself."""
-    shape, dt, dev = h.shape, h.dtype, h.device
-    rows, cols = shape
-    xt = _code(h, "h")
-    hp, ldh = _mat(h, shape, dt, dev, "h")
-    yp, ldy = _mat(dy, shape, dt, dev, "dy")
-    gp, ldg = (0, 0) if dh is None else _mat(dh, shape, dt, dev, "dh")
-    dx, dw = out if out is not None else (torch.empty(shape, dtype=dt, device=dev),
-                                          torch.empty((cols,), dtype=torch.float32, device=dev))
-    xp, ldx = _mat(dx, shape, dt, dev, "dx")
+    dx, dw = out if out is not None else (torch.empty(h.shape, dtype=h.dtype, device=h.device),
+                                          torch.empty((h.shape[1],), dtype=torch.float32, device=h.device))
     if workspace is None:
         workspace = rmsnorm_backward_workspace(h)
-    _call("fp8bs_rmsnorm_backward", dev, yp, ldy, hp, ldh, gp, ldg, xt, rows, cols, _vec(weight, cols, dev, "weight"),
-          _code(weight, "weight"), _vec32(rstd, rows, dev, "rstd"), xp, ldx, _vec32(dw, cols, dev, "dweight"),
-          *_buffer(workspace, dev, "workspace"))
+    status = (_native or _load_native()).norm_backward(dy, h, weight, rstd, dh, dx, dw, workspace)
+    if status:
+        raise Fp8bsError("fp8bs_rmsnorm_backward", status)
     return dx, dw
 
 
