@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 #include "ptx.cuh"
 #include "mx4.cuh"
+#include "ptx_fp4.cuh"
 #include "quant_kernels.cuh"
 
 namespace fp8bs {
@@ -87,6 +88,7 @@ __global__ void __launch_bounds__(256) fp4_quant_rows_kernel(const T* __restrict
     // row 16 i + 32 j past r0
     auto row_ok = [&](int i, int j) { return FULL || (col_ok && r0 + 16 * i + 32 * j < rows); };
     Vec8<T> v[2][4];
+    grid_begin();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -188,6 +190,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) fp4_quant_cols_ke
     const bool ok = FULL || (r0 < rows && c0 < cols);     // rows % 32 == 0, cols % 16 == 0
     Block8x8<T> b;
     const T* src = x + r0 * ldx + c0;
+    grid_begin();
 #pragma unroll
     for (int i = 0; i < 8; ++i, src += ldx) {
         if (!FULL) b.row[i].zero();
@@ -253,6 +256,7 @@ __global__ void __launch_bounds__(256) fp4_dequant_kernel(const uint8_t* __restr
     const uint8_t* scales = sf + ((int64_t)rb * kcs + kc) * (int64_t)kSfTileBytes + hw * 16 + ((threadIdx.x >> 2) & 3);
     T* dst = out + r0 * ldo + (kWide ? c - odd * 4 : c);
     uint32_t w[8], byte[8];
+    grid_begin();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int dr = 16 * (i & 1) + 32 * (i >> 1);

@@ -266,8 +266,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     }
     // everything above may run under the previous kernel's tail; the next one's
     // may run under this
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_begin();
 
     auto give_up = [&]() {
         *abort_flag = 1;

@@ -5,6 +5,25 @@
 
 namespace {
 
+// A launch that may be set up under the tail of the kernel before it (every kernel
+// launched so waits for it (griddepcontrol.wait) before it touches memory).
+template <typename... P, typename... A>
+fp8bs_status launch_early(void (*k)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...) != cudaSuccess) return FP8BS_ERR_CUDA;
+    return launch_status();
+}
+
 inline int64_t round32(int64_t v) { return (v + 31) / 32 * 32; }
 
 // ---------------------------------------------------------------- RMS norm
@@ -62,19 +81,15 @@ fp8bs_status launch_norm_rows(DeviceInfo* d, const NormParams& p, cudaStream_t s
     // groups' own work is spread
     RowShape sh = {(int)round32(eights), 1};
     if (p.rows > 2 * d->num_sms || eights > 1024) sh = row_shape(eights, 512, {4, 2, 1});
-    if (sh.vpt == 0) {
-        rmsnorm_quant_wide_kernel<T, BITS><<<(unsigned)p.rows, 512, 0, stream>>>(p);
-        return launch_status();
-    }
+    if (sh.vpt == 0) return launch_early(rmsnorm_quant_wide_kernel<T, BITS>, (unsigned)p.rows, 512, 0, stream, p);
     const int ty = (int)std::max<int64_t>(1, std::min<int64_t>({256 / sh.tx, p.rows, sh.tx > 32 ? 8 : 16}));
     const dim3 block((unsigned)sh.tx, (unsigned)(sh.tx == 16 ? (ty + 1) / 2 * 2 : ty));
     const unsigned grid = (unsigned)cdiv(p.rows, block.y);
     const bool full = p.cols == 8 * (int64_t)sh.vpt * sh.tx && p.rows % block.y == 0;
-    if (sh.vpt == 1) rmsnorm_quant_kernel<T, W, BITS, 1, false><<<grid, block, 0, stream>>>(p);
-    else if (sh.vpt == 2) rmsnorm_quant_kernel<T, W, BITS, 2, false><<<grid, block, 0, stream>>>(p);
-    else if (!full) rmsnorm_quant_kernel<T, W, BITS, 4, false><<<grid, block, 0, stream>>>(p);
-    else rmsnorm_quant_kernel<T, W, BITS, 4, true><<<grid, block, 0, stream>>>(p);
-    return launch_status();
+    auto k = sh.vpt == 1 ? rmsnorm_quant_kernel<T, W, BITS, 1, false>
+             : sh.vpt == 2 ? rmsnorm_quant_kernel<T, W, BITS, 2, false>
+             : !full ? rmsnorm_quant_kernel<T, W, BITS, 4, false> : rmsnorm_quant_kernel<T, W, BITS, 4, true>;
+    return launch_early(k, grid, block, 0, stream, p);
 }
 
 template <int BITS>
@@ -161,8 +176,7 @@ fp8bs_status launch_back_ring(DeviceInfo* d, const BackPlan& b, const NormBackPa
     g.ty = b.ty;
     g.slots = b.slots;
     g.err = d->err_ptr;
-    k<<<(unsigned)b.grid, g.tx * g.ty, b.smem, stream>>>(p, g);
-    return launch_status();
+    return launch_early(k, (unsigned)b.grid, (unsigned)(g.tx * g.ty), b.smem, stream, p, g);
 }
 
 template <typename T, bool WREG>
@@ -186,28 +200,17 @@ fp8bs_status launch_norm_back(DeviceInfo* d, const BackPlan& b, const NormBackPa
 {
     fp8bs_status st;
     if (b.shape.vpt == 0) {
-        rmsnorm_back_dot_kernel<T><<<(unsigned)p.rows, 512, 0, stream>>>(p);
-        rmsnorm_back_wide_kernel<T><<<dim3((unsigned)cdiv(p.cols, 2048), (unsigned)b.grid), 256, 0, stream>>>(p);
-        st = launch_status();
+        st = launch_early(rmsnorm_back_dot_kernel<T>, (unsigned)p.rows, 512, 0, stream, p);
+        if (st == FP8BS_OK)
+            st = launch_early(rmsnorm_back_wide_kernel<T>, dim3((unsigned)cdiv(p.cols, 2048), (unsigned)b.grid), 256, 0,
+                              stream, p);
     } else {
         st = (p.w_f32 != 0) == (sizeof(T) == 4) ? launch_back_rows<T, true>(d, b, p, stream)
                                                 : launch_back_rows<T, false>(d, b, p, stream);
     }
     if (st != FP8BS_OK) return st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)cdiv(p.cols, 32), 1, 1);
-    cfg.blockDim = dim3(512, 1, 1);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const float* part = p.part;
-    const int parts = (int)b.parts;
-    const int64_t cols = p.cols;
-    if (cudaLaunchKernelEx(&cfg, rmsnorm_dw_kernel, part, parts, cols, dweight) != cudaSuccess) return FP8BS_ERR_CUDA;
-    return launch_status();
+    return launch_early(rmsnorm_dw_kernel, (unsigned)cdiv(p.cols, 32), 512, 0, stream, (const float*)p.part, (int)b.parts,
+                        p.cols, dweight);
 }
 
 // ---------------------------------------------------------------- 4-bit product
@@ -386,18 +389,8 @@ fp8bs_status launch_reduce(DeviceInfo* d, const float* ws, int splits, int64_t M
 {
     const int64_t chunks = M * ((N + 3) / 4);
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(chunks, kReduceThreads), (int64_t)d->num_sms * 16));
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = dim3(kReduceThreads, 1, 1);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, splitk_reduce_kernel, ws, splits, M, N, ldw, D, ldd, out_f32, vec_out) != cudaSuccess)
-        return FP8BS_ERR_CUDA;
-    return launch_status();
+    return launch_early(splitk_reduce_kernel, grid, kReduceThreads, 0, stream, ws, splits, M, N, ldw, D, ldd, out_f32,
+                        vec_out);
 }
 
 }  // namespace
@@ -504,23 +497,17 @@ fp8bs_status fp4_quant_1x32(const void* x, fp8bs_dtype xt, int64_t rows, int64_t
     if (tiles > INT32_MAX) return FP8BS_ERR_INVALID_ARG;
     const bool full = rows % (transpose_out ? kQ4Rows : 128) == 0 && cols % (transpose_out ? kQ4Cols : 128) == 0;
     auto launch = [&](auto kernel, auto* p, auto... more) {
-        kernel<<<(unsigned)tiles, 256, 0, stream>>>(p, rows, cols, ldx, q, ldq, scale_tiles, (int)kcs, more...);
+        return launch_early(kernel, (unsigned)tiles, 256, 0, stream, p, rows, cols, ldx, q, ldq, scale_tiles, (int)kcs,
+                            more...);
     };
     const int tc = (int)tiles_c;
-    if (xt == FP8BS_BF16) {
-        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(x);
-        if (!transpose_out && full) launch(fp4_quant_rows_kernel<__nv_bfloat16, true>, p);
-        else if (!transpose_out) launch(fp4_quant_rows_kernel<__nv_bfloat16, false>, p);
-        else if (full) launch(fp4_quant_cols_kernel<__nv_bfloat16, true>, p, tc);
-        else launch(fp4_quant_cols_kernel<__nv_bfloat16, false>, p, tc);
-    } else {
-        const float* p = static_cast<const float*>(x);
-        if (!transpose_out && full) launch(fp4_quant_rows_kernel<float, true>, p);
-        else if (!transpose_out) launch(fp4_quant_rows_kernel<float, false>, p);
-        else if (full) launch(fp4_quant_cols_kernel<float, true>, p, tc);
-        else launch(fp4_quant_cols_kernel<float, false>, p, tc);
-    }
-    return launch_status();
+    auto typed = [&](auto* p) {
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+        if (transpose_out)
+            return full ? launch(fp4_quant_cols_kernel<T, true>, p, tc) : launch(fp4_quant_cols_kernel<T, false>, p, tc);
+        return full ? launch(fp4_quant_rows_kernel<T, true>, p) : launch(fp4_quant_rows_kernel<T, false>, p);
+    };
+    return xt == FP8BS_BF16 ? typed(static_cast<const __nv_bfloat16*>(x)) : typed(static_cast<const float*>(x));
 }
 
 fp8bs_status fp4_dequant_1x32(const uint8_t* q, int64_t ldq, const uint8_t* scale_tiles, int64_t rows, int64_t cols,
@@ -540,19 +527,12 @@ fp8bs_status fp4_dequant_1x32(const uint8_t* q, int64_t ldq, const uint8_t* scal
     if (tiles > INT32_MAX) return FP8BS_ERR_INVALID_ARG;
     const unsigned grid = (unsigned)tiles;
     const bool full = rows % 128 == 0 && cols % 128 == 0;
-    auto launch = [&](auto kernel, auto* p) {
-        kernel<<<grid, 256, 0, stream>>>(q, ldq, scale_tiles, rows, cols, (int)cdiv(cols, 128), p, ldo);
+    auto typed = [&](auto* p) {
+        using T = std::remove_pointer_t<decltype(p)>;
+        return launch_early(full ? fp4_dequant_kernel<T, true> : fp4_dequant_kernel<T, false>, grid, 256, 0, stream, q, ldq,
+                            scale_tiles, rows, cols, (int)cdiv(cols, 128), p, ldo);
     };
-    if (ot == FP8BS_BF16) {
-        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(out);
-        if (full) launch(fp4_dequant_kernel<__nv_bfloat16, true>, p);
-        else launch(fp4_dequant_kernel<__nv_bfloat16, false>, p);
-    } else {
-        float* p = static_cast<float*>(out);
-        if (full) launch(fp4_dequant_kernel<float, true>, p);
-        else launch(fp4_dequant_kernel<float, false>, p);
-    }
-    return launch_status();
+    return ot == FP8BS_BF16 ? typed(static_cast<__nv_bfloat16*>(out)) : typed(static_cast<float*>(out));
 }
 
 size_t fp4_scaled_gemm_workspace_size(int64_t M, int64_t N, int64_t K)

@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_quant_kernel(co
     auto inside = [&](int c) { return FULL || (row_ok && c < p.cols); };
     Vec8<T> a[VPT];
     float ss = 0.f;
+    grid_begin();
     {
         const T* src = static_cast<const T*>(p.x) + r * p.ldx;
 #pragma unroll
@@ -364,6 +365,7 @@ __device__ __forceinline__ RingView ring_init(const RowRing& g, uint8_t* smem, i
         fence_barrier_init();
     }
     __syncthreads();
+    grid_begin();
     if (threadIdx.x < 32)
         for (int s = 0; s < g.slots; ++s)
             if (blockIdx.x + (int64_t)s * gridDim.x < blocks) ring_issue(g, v, blockIdx.x + (int64_t)s * gridDim.x, s);
@@ -433,6 +435,7 @@ __global__ void __launch_bounds__(512) rmsnorm_quant_wide_kernel(const NormParam
     const T* res = static_cast<const T*>(p.res) + r * p.ldr;
     T* h = static_cast<T*>(p.h) + r * p.ldh;
     float ss = 0.f;
+    grid_begin();
     for (int64_t c = (int64_t)threadIdx.x * 8; c < p.cols; c += (int64_t)blockDim.x * 8) {
         Vec8<T> a;
         a.load(x + c);
@@ -493,8 +496,6 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) rmsnorm_back_kernel(co
     __shared__ __align__(16) float part[2][16];
     const int64_t blocks = (g.rows + g.ty - 1) / g.ty;
     const RingView v = ring_init(g, ring_raw, blocks);
-    // the reduction that follows may be set up from here on
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int y = (int)threadIdx.x / g.tx, x = (int)threadIdx.x - y * g.tx;
     Eight dw[VPT];
 #pragma unroll
@@ -593,6 +594,7 @@ __global__ void __launch_bounds__(512) rmsnorm_back_dot_kernel(const NormBackPar
 {
     const int64_t r = blockIdx.x;
     float2 dot2 = make_float2(0.f, 0.f);
+    grid_begin();
     for (int64_t c = (int64_t)threadIdx.x * 8; c < p.cols; c += (int64_t)blockDim.x * 8) {
         Vec8<T> a, b;
         a.load(static_cast<const T*>(p.dy) + r * p.lddy + c);
@@ -612,6 +614,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) rmsnorm_back_wide_kernel(const NormBackParams p)
 {
     const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    grid_begin();
     if (c >= p.cols) return;
     const Eight w = load_weight8(p.w, p.w_f32, c);
     Eight dw = eight_zero();
@@ -636,15 +639,14 @@ __global__ void __launch_bounds__(256) rmsnorm_back_wide_kernel(const NormBackPa
 }
 
 // dw[c] = sum over the parts, 32 columns a CTA: warp w adds parts w, w + 16, ..,
-// eight loads in flight, and the warps' sums are added in order.  A programmatic
-// dependent of the pass that leaves the parts.
+// eight loads in flight, and the warps' sums are added in order.
 __global__ void __launch_bounds__(512) rmsnorm_dw_kernel(const float* __restrict__ part, int parts, int64_t cols,
                                                          float* __restrict__ dw)
 {
     __shared__ float s[16][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_begin();
     float sum = 0.f;
     if (c < cols) {
         for (int i = warp; i < parts; i += 128) {

@@ -55,6 +55,15 @@ __device__ __forceinline__ void umma_f4_bs_pair(uint32_t d_tmem, uint64_t adesc,
         : "memory");
 }
 
+// Programmatic launches: waits until the kernels before this one have completed
+// and their results are visible, then lets the next one be set up on SMs with
+// room; before it no kernel touches memory that another may write.
+__device__ __forceinline__ void grid_begin()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Thread i of the warp writes 16 consecutive columns of TMEM lane
 // lane_base + i; complete after tmem_st_wait.
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t* r)
