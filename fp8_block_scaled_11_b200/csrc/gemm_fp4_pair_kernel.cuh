@@ -125,6 +125,7 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_const
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    grid_begin();
 
     auto give_up = [&]() {
         *abort_flag = 1;

@@ -348,11 +348,13 @@ fp8bs_status launch_fp4_pair(DeviceInfo* d, const CUtensorMap& tW, const CUtenso
                       (uint64_t)p.kcs * kSfTileBytes, 256, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (st != FP8BS_OK) return st;
     auto k = gemm_fp4_pair_kernel;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kF4PairThreads, 1, 1);
     cfg.dynamicSmemBytes = Fp4PairSmem::alloc;
@@ -379,6 +381,7 @@ fp8bs_status launch_fp4_pair(DeviceInfo* d, const CUtensorMap& tW, const CUtenso
         }
     }
     cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(p.num_units, nc)), 1, 1);
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, k, tW, tT, tSW, tST, p) != cudaSuccess) return FP8BS_ERR_CUDA;
     return launch_status();
 }
