@@ -224,51 +224,63 @@ struct Fp4Plan {
     size_t ws_bytes;
 };
 
+// What a product takes on single CTAs, in us: units (a tile's part of K) over SMs
+// that hold two, each round of them the tile's fixed part and its steps of 256 K,
+// where a round leaves an SM to each unit (`fixed`, `step`) or puts two on it
+// (`fixed2`, `step2`), and what sending and adding a cluster's sums adds.
+struct Fp4Cost {
+    double fixed, step, fixed2, step2, send, send2;
+};
+
+double fp4_single_us(const Fp4Cost& c, int64_t units, int64_t steps, bool send, int num_sms)
+{
+    const int64_t room = 2 * num_sms, rounds = units / room, rest = units % room;
+    double us = (double)rounds * (c.fixed2 + c.step2 * (double)steps);
+    if (rest > num_sms) us += c.fixed2 + c.step2 * (double)steps;
+    else if (rest > 0) us += c.fixed + c.step * (double)steps;
+    return us + (!send ? 0. : units > num_sms ? c.send2 : c.send);
+}
+
+// Tiles and the split of K: the fastest of CTA pairs and of single CTAs with each
+// tile width and cluster size, by models of their times fitted to 600 measured
+// ones (M 130 .. 4096, N 1000 .. 32000, K 256 .. 8192), where the choice costs
+// 0.6% over the fastest in the mean and 14% at most.  Measured: 1024 x 5120 x 8192
+// 24.7 us on pairs, 31.5 on single CTAs of 128 columns; 512 x 8192 x 256 4.6 with
+// 128 columns, 7.4 with 64; 256 x 2080 x 8192 10.3 with 64 columns over clusters of
+// four, 13.6 on pairs; 72 x 5120 x 8192 9.0 over clusters of four, 14.2 without.
 Fp4Plan plan_fp4(int64_t M, int64_t N, int64_t K, int num_sms)
 {
-    Fp4Plan s;
-    // CTA pairs, or single CTAs with 128 x 128 tiles once those are more than the
-    // SMs: by what each takes in us, waves of tiles (for single CTAs, which share an
-    // SM: tiles per SM) times a tile's fixed part and its steps of 256 K.  Fitted to
-    // M 200 .. 16640, N 151 .. 32000, K 256 .. 8192, where the choice costs 1% over
-    // the better one in the mean.  Measured: 2048 x 4096 x 256 8.5 us on either, x
-    // 1024 10.0 on pairs and 11.1 on single CTAs, x 4096 17.1 and 21.1; 16640 x 5120
-    // x 512 53 and 100; 1536 x 4096 x 256 8.4 and 7.4.
+    static constexpr Fp4Cost kCost[4] = {{0.2, 0.30, 0.2, 0.30, 0.35, 0.5},       // 16 columns
+                                         {0.4, 0.30, 0.4, 0.30, 0.7, 1.0},        // 32
+                                         {2.1, 0.38, 2.8, 0.41, 1.3, 1.8},        // 64
+                                         {2.5, 0.39, 3.3, 0.45, 2.6, 3.2}};       // 128
+    Fp4Plan s = {};
     const int64_t steps = cdiv(K, kF4StepK);
-    const int64_t t_pair = cdiv(M, kF4Pair) * cdiv(N, kF4Pair), t_one = cdiv(M, 128) * cdiv(N, kF4Rows);
-    const double pair_us = 4.5 + (double)cdiv(t_pair, std::max(1, num_sms / 2)) * (1.8 + 0.31 * (double)steps);
-    const double one_us = 1.35 + (double)t_one / num_sms * (1.91 + 0.275 * (double)steps);
-    s.pair = M > 128 && t_one > num_sms && pair_us < one_us;
-    s.tiles_n = (int)cdiv(N, s.pair ? kF4Pair : kF4Rows);
+    s.tiles_n = (int)cdiv(N, kF4Rows);
     s.parts = 1;
     s.splits = 1;
-    if (s.pair) {
-        s.bn = kF4Pair;
-    } else {
-        // single CTAs: the narrowest tile that holds every token, or either of the two
-        // widest ones; and K over the CTAs of a cluster where its shorter share of
-        // steps (256 K) pays for sending and adding the sums.  By what a unit takes in
-        // us, two per SM: 5120 x 8192 takes 9.0 at 72 tokens (four parts, 128 columns;
-        // one part 14.2), 13.8 at 256 (two parts, 128 columns; one 15.3, with 64
-        // columns 15.6); 1000 x 2080 5.0 at 256 (four parts, 64 columns; one 6.0), 6.2
-        // at 777 (one part, 64 columns; two 7.6, with 128 columns 7.0).
-        const int widest = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-        double best = 1e30;
-        for (int bn = std::min(widest, 64); bn <= widest; bn *= 2) {
-            const int64_t units = cdiv(M, bn) * s.tiles_n;
-            const double step = bn <= 32 ? 0.3 : bn == 64 ? 0.42 : 0.5;
-            for (int parts = 1; parts <= kF4MaxCluster; parts *= 2) {
-                if (parts > 1 && (units * parts > 2 * num_sms || steps < 2 * parts)) break;
-                double us = (double)cdiv(steps, parts) * step * (double)cdiv(units * parts, 2 * num_sms);
-                if (parts == 1) us += 0.012 * bn;
-                else us += 0.034 * bn * (units * parts > num_sms ? 1.3 : 1.0);
-                if (us < best) {
-                    best = us;
-                    s.bn = bn;
-                    s.parts = parts;
-                }
+    double best = 1e30;
+    // the narrowest tile that holds every token, or either of the two widest ones
+    for (int i = M <= 16 ? 0 : M <= 32 ? 1 : 2, bn = 16 << i; i < 4; ++i, bn *= 2) {
+        const int64_t units = cdiv(M, bn) * s.tiles_n;
+        for (int parts = 1; parts <= kF4MaxCluster; parts *= 2) {
+            if (parts > 1 && (units * parts > 2 * num_sms || steps < 2 * parts)) break;
+            const double us = fp4_single_us(kCost[i], units * parts, cdiv(steps, parts), parts > 1, num_sms);
+            if (us < best) {
+                best = us;
+                s.bn = bn;
+                s.parts = parts;
             }
         }
+        if (M <= bn) break;
+    }
+    const int64_t waves = cdiv(cdiv(M, kF4Pair) * cdiv(N, kF4Pair), std::max(1, num_sms / 2));
+    s.pair = M > 128 && 2.85 + (double)waves * (1.48 + 0.308 * (double)steps) < best;
+    if (s.pair) {
+        s.bn = kF4Pair;
+        s.tiles_n = (int)cdiv(N, kF4Pair);
+        s.parts = 1;
+    } else {
         // very long K over clusters too, where they leave half of the room and 8 steps a CTA
         const int64_t ctas = cdiv(M, s.bn) * s.tiles_n * s.parts;
         if (s.parts == kF4MaxCluster)

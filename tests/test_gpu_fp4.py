@@ -166,7 +166,8 @@ SHAPES = [(1, 1, 32), (1, 5120, 8192), (7, 130, 96), (16, 128, 256), (17, 1000, 
           (65, 300, 160), (128, 128, 2048), (129, 384, 1056), (200, 640, 224), (256, 4096, 1024), (300, 1000, 2080),
           (777, 1000, 2080), (1024, 19000, 64), (129, 19000, 96), (2300, 2304, 288),
           (5000, 1100, 544), (2305, 2050, 4128), (70, 19000, 160), (1, 100, 1056), (5, 100, 2080), (20, 130, 2080),
-          (40, 100, 2080), (65, 100, 4128), (500, 520, 8224), (4000, 2050, 96)]
+          (40, 100, 2080), (65, 100, 4128), (500, 520, 8224), (4000, 2050, 96), (20, 100, 4128), (300, 4100, 8192),
+          (1500, 130, 16416)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -259,8 +260,8 @@ def test_product_nan_scale_stays_in_its_row():
     check(d[keep], av[keep], bv, torch.float32, K)
 
 
-def test_product_long_k():
-    M, N, K = 24, 256, 65536 + 32
+@pytest.mark.parametrize("M,N,K", [(24, 256, 65536 + 32), (1, 130, 131072), (100, 100, 65536), (300, 100, 70016)])
+def test_product_long_k(M, N, K):
     a, sa, av = operand(M, K, 31, spread=2)
     b, sb, bv = operand(N, K, 32, spread=2)
     d = ops.fp4_scaled_gemm(a, b, sa, sb, out_dtype=torch.float32)
