@@ -209,7 +209,7 @@ fp8bs_status launch_norm_back(DeviceInfo* d, const BackPlan& b, const NormBackPa
                                                 : launch_back_rows<T, false>(d, b, p, stream);
     }
     if (st != FP8BS_OK) return st;
-    return launch_early(rmsnorm_dw_kernel, (unsigned)cdiv(p.cols, 32), 512, 0, stream, (const float*)p.part, (int)b.parts,
+    return launch_early(rmsnorm_dw_kernel, (unsigned)cdiv(p.cols, 32), 32 * kDwWarps, 0, stream, (const float*)p.part, (int)b.parts,
                         p.cols, dweight);
 }
 

@@ -638,33 +638,37 @@ __global__ void __launch_bounds__(256) rmsnorm_back_wide_kernel(const NormBackPa
     store8(p.part + (int64_t)blockIdx.y * p.cols + c, dw);
 }
 
-// dw[c] = sum over the parts, 32 columns a CTA: warp w adds parts w, w + 16, ..,
-// eight loads in flight, and the warps' sums are added in order.
-__global__ void __launch_bounds__(512) rmsnorm_dw_kernel(const float* __restrict__ part, int parts, int64_t cols,
-                                                         float* __restrict__ dw)
+// dw[c] = sum over the parts, 32 columns a CTA: warp w adds parts w, w + 32, ..,
+// ten loads in flight (the usual two parts an SM in one round trip to L2), and the
+// warps' sums are added in a tree.
+constexpr int kDwWarps = 32;
+
+__global__ void __launch_bounds__(32 * kDwWarps) rmsnorm_dw_kernel(const float* __restrict__ part, int parts, int64_t cols,
+                                                                   float* __restrict__ dw)
 {
-    __shared__ float s[16][32];
+    __shared__ float s[kDwWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     grid_begin();
     float sum = 0.f;
     if (c < cols) {
-        for (int i = warp; i < parts; i += 128) {
-            float v[8];
+        for (int i = warp; i < parts; i += 10 * kDwWarps) {
+            float v[10];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = i + 16 * j < parts ? __ldcg(part + (int64_t)(i + 16 * j) * cols + c) : 0.f;
+            for (int j = 0; j < 10; ++j)
+                v[j] = i + kDwWarps * j < parts ? __ldcg(part + (int64_t)(i + kDwWarps * j) * cols + c) : 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum += v[j];
+            for (int j = 0; j < 10; ++j) sum += v[j];
         }
     }
     s[warp][lane] = sum;
     __syncthreads();
-    if (warp == 0 && c < cols) {
-        float t = s[0][lane];
+    // warp w adds column w's sums: lane l holds warp l's
+    float t = s[lane][warp];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) t += s[i][lane];
-        dw[c] = t;
-    }
+    for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    const int64_t col = (int64_t)blockIdx.x * 32 + warp;
+    if (lane == 0 && col < cols) dw[col] = t;
 }
 
 }  // namespace fp8bs
