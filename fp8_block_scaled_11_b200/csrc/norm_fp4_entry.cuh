@@ -57,13 +57,14 @@ struct RowShape {
     int tx, vpt;                // vpt == 0: the row is too wide
 };
 
+inline int64_t round_row(int64_t tx) { return tx <= 16 ? 16 : round32(tx); }
+
 RowShape row_shape(int64_t eights, int64_t max_tx, const int (&order)[3])
 {
     RowShape best = {0, 0};
     int64_t best_idle = INT64_MAX;
     for (int vpt : order) {
-        int64_t tx = cdiv(eights, vpt);
-        tx = tx <= 16 ? 16 : round32(tx);
+        const int64_t tx = round_row(cdiv(eights, vpt));
         if (tx <= max_tx && tx * vpt - eights < best_idle) {
             best_idle = tx * vpt - eights;
             best = {(int)tx, vpt};
@@ -120,19 +121,24 @@ BackPlan plan_back(int64_t rows, int64_t cols, int64_t elem, int mats, int num_s
     BackPlan b = {};
     const int64_t eights = cdiv(cols, 8);
     const uint32_t row_bytes = (uint32_t)std::min<int64_t>(cols * elem, kRingSmem);
-    // four, two or one eights per thread: what keeps the most threads of an SM at
-    // work, 512 at most, over CTAs of 256 (or of one row's) that each have room
-    // for two slots; more eights a thread among equals
+    // eights per thread: one where 16 threads hold a row (100000 x 128 bf16 21 us, with
+    // two 26), over 1024 threads of an SM; else four or two over 512, whichever keeps
+    // more of them at work.  Among equals four (16640 x 1616 bf16 39 us, with two 47),
+    // but two where the SMs have under three rows each, whose latency counts (161 x
+    // 3776 bf16 6.0 us, with four 6.2; 333 x 1040 fp32 5.8 and 6.4).  A CTA has 256
+    // threads (or one row's) and room for two slots.
     double best = 0.;
-    for (int vpt = 4; vpt >= 1; vpt /= 2) {
-        int64_t tx = cdiv(eights, vpt);
-        tx = tx <= 16 ? 16 : round32(tx);
+    for (int i = 0; i < 2; ++i) {
+        const bool narrow = eights <= 16;
+        const bool two_first = rows < 3 * num_sms && eights <= 512;     // (at most 256 threads a row)
+        const int vpt = narrow ? 1 : two_first == (i == 0) ? 2 : 4;
+        const int64_t tx = narrow ? 16 : round_row(cdiv(eights, vpt));
         if (tx > 512) continue;
         int ty = std::max(1, (int)(256 / tx));
         while (ty > 1 && cdiv(rows, ty) < num_sms) ty /= 2;             // few rows: over more SMs
         if (tx == 16) ty = (ty + 1) / 2 * 2;                            // whole warps
         const uint32_t slot = ring_smem(row_bytes, ty, mats, 1);
-        const int per_sm = (int)std::min<int64_t>(512 / (tx * ty), kRingSmem / (2 * slot + 1024));
+        const int per_sm = (int)std::min<int64_t>((narrow ? 1024 : 512) / (tx * ty), kRingSmem / (2 * slot + 1024));
         const double busy = (double)per_sm * (double)ty * (double)eights / vpt;
         if (per_sm < 1 || busy <= best) continue;
         best = busy;

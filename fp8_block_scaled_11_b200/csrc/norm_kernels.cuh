@@ -490,7 +490,7 @@ struct NormBackParams {
 // `part`.  Two CTAs of 256 threads an SM hide each other's sums and barriers: one
 // of 512, over two rows at a time, took 247 us where two took 195.
 template <typename T, int VPT, int THREADS, bool WREG>
-__global__ void __launch_bounds__(THREADS, 512 / THREADS) rmsnorm_back_kernel(const NormBackParams p, const RowRing g)
+__global__ void __launch_bounds__(THREADS, (VPT == 1 ? 1024 : 512) / THREADS) rmsnorm_back_kernel(const NormBackParams p, const RowRing g)
 {
     extern __shared__ __align__(128) uint8_t ring_raw[];
     __shared__ __align__(16) float part[2][16];
