@@ -27,6 +27,11 @@
 // them have completed: the writers follow a refill, which follows the commit.
 // TMEM: the 256-column accumulator, then kF4PairStages x 48 scale columns.
 //
+// 16640 x 5120 x 8192 takes 226-242 us (5.8-6.2 PFLOP/s; the tensor pipe is busy 86%
+// of the time) and 270 in a long row of calls, under the power cap.  A tile's
+// fixed 1.5 us (the accumulator's way out before the next tile may start: TMEM
+// has no room for a second one beside the scale factors) is what short K pays.
+//
 // Every wait is bounded as in gemm_pair_kernel.cuh; a wait that runs out stops
 // both CTAs' roles.
 #pragma once

@@ -538,8 +538,8 @@ fp8bs_status fp4_dequant_1x32(const uint8_t* q, int64_t ldq, const uint8_t* scal
  *              beyond what a cluster of CTAs shares: NULL/0 to do without, or at
  *              least fp4_scaled_gemm_workspace_size(M, N, K) bytes (0 for most
  *              sizes), 16-byte aligned.  Partial sums are added in a fixed order:
- *              results are deterministic on one kind of device.  Calls that may overlap on the GPU need a
- *              workspace each.
+ *              results are deterministic on one kind of device.  Calls that may
+ *              overlap on the GPU need a workspace each.
  * Any M, N >= 1; K >= 32, K % 32 == 0.  A, Bt, scale_a, scale_b 16-byte aligned;
  * lda, ldb multiples of 16; D aligned to its element size.
  */
