@@ -77,3 +77,100 @@ def test_eight_threads_and_streams():
     r = subprocess.run([sys.executable, "-c", SCRIPT, ROOT], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stderr[-2000:]
     assert "threads ok" in r.stdout
+
+
+@pytest.mark.parametrize("M", [1, 40, 300, 2300])
+def test_chain_without_waits(M):
+    """Sixty steps of dependent calls over the same buffers, each written again as soon as the call that reads it is
+    launched: the same bits with the host waiting after every call, without waiting, and from a replayed graph."""
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from fp8_block_scaled_11_b200 import build, inputs, ops
+    build.build()
+    K = 1024
+    x0 = inputs.random_matrix(M, K, seed=81).cuda()
+    wq, ws = ops.fp4_quant_1x32(inputs.random_matrix(K, K, seed=82, scale=K ** -0.5).cuda())
+    g = torch.linspace(0.5, 1.5, K, device="cuda").bfloat16()
+    x, r = torch.empty_like(x0), torch.empty_like(x0)
+    out4, out8 = ops.rmsnorm_quant_buffers(x0, residual=True, bits=4), ops.rmsnorm_quant_buffers(x0, want_y=True)
+    q, s = ops.fp4_quant_1x32(x0)
+    dx, dw = torch.empty_like(x0), torch.empty(K, device="cuda")
+    total = torch.empty(K, device="cuda")
+    bwd = ops.rmsnorm_backward_workspace(x0)
+
+    def steps(wait):
+        x.copy_(x0)
+        r.copy_(x0)
+        total.zero_()
+        for _ in range(60):
+            _, _, h, rstd, _ = ops.fp4_rmsnorm_quant_1x32(x, g, residual=r, out=out4)
+            wait()
+            ops.fp4_scaled_gemm(out4[0], wq, out4[1], ws, out=x)
+            wait()
+            ops.fp4_quant_1x32(x, q=q, scale=s)
+            wait()
+            ops.fp4_dequant_1x32(q, s, out=r)
+            wait()
+            y = ops.fp8_rmsnorm_quant_1x128(r, g, out=out8)[4]
+            wait()
+            ops.fp8bs_rmsnorm_backward(y, h, g, rstd, dh=x, out=(dx, dw), workspace=bwd)
+            wait()
+            total.add_(dw)
+            r.add_(dx, alpha=0.5)
+            wait()
+        return [t.clone() for t in (x, r, total, out8[0], dx)]
+
+    want = steps(torch.cuda.synchronize)
+    assert all(bool(torch.isfinite(t.float()).all()) for t in want)
+    got = steps(lambda: None)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = steps(lambda: None)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+FIRST = r'''
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch
+from fp8_block_scaled_11_b200 import build, inputs, ops
+
+build.build()
+x = inputs.random_matrix(600, 1024, seed=91).cuda()
+w = torch.ones(1024, device="cuda").bfloat16()
+
+def calls():
+    out = []
+    for m in (1, 600):
+        q, s, h, rstd, y = ops.fp4_rmsnorm_quant_1x32(x[:m], w, x[:m], want_y=True)
+        wq, ws = ops.fp4_quant_1x32(x)
+        out += [q, ops.fp4_scaled_gemm(q, wq, s, ws), *ops.fp8bs_rmsnorm_backward(y, h, w, rstd)]
+    big = torch.cat([x] * 8)
+    bq, bs = ops.fp4_quant_1x32(big)
+    return out + [ops.fp4_scaled_gemm(bq, bq, bs, bs)]           # CTA pairs
+
+torch.cuda.synchronize()
+side = torch.cuda.Stream()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=side):
+    got = calls()
+g.replay()
+torch.cuda.synchronize()
+assert ops.fp8bs_check_device_error() == 0
+for a, b in zip(got, calls()):
+    assert torch.equal(a, b)
+print("captured ok")
+'''
+
+
+def test_first_calls_inside_a_capture():
+    """The library's very first use of each kernel may be inside a graph's capture."""
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    r = subprocess.run([sys.executable, "-c", FIRST, ROOT], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and "captured ok" in r.stdout, r.stderr[-2000:]
