@@ -606,6 +606,8 @@ fp8bs_status fp4_scaled_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* A, 
     p.band = (int32_t)std::min<int64_t>(
         plan.tiles_n, std::max<int64_t>(4, (int64_t)(32 << 20) / ((plan.pair ? kF4Pair : kF4Rows) * cdiv(K, 2))));
     p.num_units = (int64_t)plan.tiles_m * plan.tiles_n * plan.splits;
+    p.B = Bt;
+    p.ldb = ldb;
     p.sfa = scale_a;
     p.sfb = scale_b;
     p.D = D;

@@ -64,6 +64,13 @@ __device__ __forceinline__ void grid_begin()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// The 128-byte line at p into L2 only, which stays coherent: allowed before
+// grid_begin whoever writes the data.
+__device__ __forceinline__ void prefetch_l2(const void* p)
+{
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
 // Thread i of the warp writes 16 consecutive columns of TMEM lane
 // lane_base + i; complete after tmem_st_wait.
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t* r)
