@@ -49,7 +49,7 @@ struct DeviceInfo {
     std::atomic<bool> tile_attr_set[16]{};   // per tile kernel kind (+8: power-of-two scale rule)
     std::atomic<int> tile_blocks[16]{};
     std::atomic<int> pair_clusters[8]{};     // co-resident CTA pairs, per pair-kernel instantiation
-    std::atomic<bool> ring_attr_set[24]{};   // RMS norm backward, per instantiation
+    std::atomic<bool> ring_attr_set[32]{};   // RMS norm backward, per instantiation
     std::atomic<bool> fp4_attr_set[4]{};     // 4-bit product on single CTAs, per tile width
     std::atomic<int> fp4_clusters[4][4]{};   // and co-resident clusters of 2^i CTAs
     std::atomic<int> fp4_pair_clusters{};    // 4-bit product on CTA pairs: co-resident pairs

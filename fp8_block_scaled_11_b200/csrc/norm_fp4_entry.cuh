@@ -8,20 +8,31 @@ namespace {
 // A launch that may be set up under the tail of the kernel before it (every kernel
 // launched so waits for it (griddepcontrol.wait) before it touches memory).
 template <typename... P, typename... A>
-fp8bs_status launch_early(void (*k)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args)
+fp8bs_status launch_early_cluster(void (*k)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, int cluster,
+                                  A... args)
 {
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...) != cudaSuccess) return FP8BS_ERR_CUDA;
     return launch_status();
+}
+
+template <typename... P, typename... A>
+fp8bs_status launch_early(void (*k)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args)
+{
+    return launch_early_cluster(k, grid, block, smem, stream, 1, args...);
 }
 
 inline int64_t round32(int64_t v) { return (v + 31) / 32 * 32; }
@@ -109,12 +120,14 @@ fp8bs_status launch_norm(DeviceInfo* d, const NormParams& p, fp8bs_dtype xt, cud
 struct BackPlan {
     RowShape shape;             // vpt == 0: wide rows
     int ty, slots, per_sm;      // rows per block of the ring, its depth, CTAs per SM
+    int cluster;                // CTAs of the one cluster that takes all rows (0: many CTAs, and a second launch)
     uint32_t smem;
     int64_t grid, parts;
     size_t dot_off, bytes;
 };
 
 constexpr uint32_t kRingSmem = 222 * 1024;      // of an SM's shared memory
+constexpr int kBackCluster = 8;                 // CTAs of a cluster, at most
 
 BackPlan plan_back(int64_t rows, int64_t cols, int64_t elem, int mats, int num_sms)
 {
@@ -153,14 +166,27 @@ BackPlan plan_back(int64_t rows, int64_t cols, int64_t elem, int mats, int num_s
     b.parts = b.grid;
     b.dot_off = (size_t)(b.parts * cols) * sizeof(float);
     b.bytes = b.dot_off + (b.shape.vpt == 0 ? (size_t)((rows + 3) / 4 * 4) * sizeof(float) : 0);
+    // few narrow rows: one cluster takes them all and adds up dw itself, without the
+    // second launch (64 x 512 bf16 4.0 us instead of 4.3, called from Python 4.6
+    // instead of 6.2; 16 x 1024 4.5 and 4.1, 5.0 and 6.1; at 4096 columns slower)
+    const int ty = b.shape.vpt > 0 ? 256 / std::min(b.shape.tx, 256) : 1;
+    const int64_t blocks = cdiv(rows, ty);
+    if ((b.shape.vpt == 1 || b.shape.vpt == 2) && blocks <= (b.shape.tx == 16 ? 2 : b.shape.tx <= 64 ? 1 : 0) * kBackCluster) {
+        b.cluster = blocks > 4 ? kBackCluster : blocks > 2 ? 4 : (int)blocks;
+        b.ty = ty;
+        b.slots = 2;
+        b.smem = ring_smem(row_bytes, ty, mats, 2);
+        b.grid = b.cluster;
+    }
     return b;
 }
 
-template <typename T, int VPT, int THREADS, bool WREG>
+template <typename T, int VPT, int THREADS, bool WREG, bool CLUSTER = false>
 fp8bs_status launch_back_ring(DeviceInfo* d, const BackPlan& b, const NormBackParams& p, cudaStream_t stream)
 {
-    auto k = rmsnorm_back_kernel<T, VPT, THREADS, WREG>;
-    constexpr int slot = (sizeof(T) == 4 ? 1 : 0) + (WREG ? 2 : 0) + (VPT >> 1) * 4 + (THREADS > 256 ? 12 : 0);
+    auto k = rmsnorm_back_kernel<T, VPT, THREADS, WREG, CLUSTER>;
+    constexpr int slot = (sizeof(T) == 4 ? 1 : 0) + (WREG ? 2 : 0) + (VPT >> 1) * 4 + (THREADS > 256 ? 12 : 0) +
+                         (CLUSTER ? 24 : 0);
     if (!d->ring_attr_set[slot].load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> lock(g_mutex);
         if (!d->ring_attr_set[slot].load(std::memory_order_relaxed)) {
@@ -182,7 +208,7 @@ fp8bs_status launch_back_ring(DeviceInfo* d, const BackPlan& b, const NormBackPa
     g.ty = b.ty;
     g.slots = b.slots;
     g.err = d->err_ptr;
-    return launch_early(k, (unsigned)b.grid, (unsigned)(g.tx * g.ty), b.smem, stream, p, g);
+    return launch_early_cluster(k, (unsigned)b.grid, (unsigned)(g.tx * g.ty), b.smem, stream, std::max(1, b.cluster), p, g);
 }
 
 template <typename T, bool WREG>
@@ -195,6 +221,9 @@ fp8bs_status launch_back_rows(DeviceInfo* d, const BackPlan& b, const NormBackPa
             if (b.shape.vpt == 2) return launch_back_ring<T, 2, 512, WREG>(d, b, p, stream);
         return launch_back_ring<T, 4, 512, WREG>(d, b, p, stream);
     }
+    if (b.cluster > 0)
+        return b.shape.vpt == 1 ? launch_back_ring<T, 1, 256, WREG, true>(d, b, p, stream)
+                                : launch_back_ring<T, 2, 256, WREG, true>(d, b, p, stream);
     if (b.shape.vpt == 1) return launch_back_ring<T, 1, 256, WREG>(d, b, p, stream);
     if (b.shape.vpt == 2) return launch_back_ring<T, 2, 256, WREG>(d, b, p, stream);
     return launch_back_ring<T, 4, 256, WREG>(d, b, p, stream);
@@ -214,7 +243,7 @@ fp8bs_status launch_norm_back(DeviceInfo* d, const BackPlan& b, const NormBackPa
         st = (p.w_f32 != 0) == (sizeof(T) == 4) ? launch_back_rows<T, true>(d, b, p, stream)
                                                 : launch_back_rows<T, false>(d, b, p, stream);
     }
-    if (st != FP8BS_OK) return st;
+    if (st != FP8BS_OK || b.cluster > 0) return st;
     return launch_early(rmsnorm_dw_kernel, (unsigned)cdiv(p.cols, 32), 32 * kDwWarps, 0, stream, (const float*)p.part, (int)b.parts,
                         p.cols, dweight);
 }
@@ -485,7 +514,7 @@ fp8bs_status fp8bs_rmsnorm_backward(const void* dy, int64_t lddy, const void* h,
     if (workspace == nullptr || workspace_bytes < fp8bs_rmsnorm_backward_workspace_size(rows, cols))
         return FP8BS_ERR_WORKSPACE;
     if (!aligned16(workspace)) return FP8BS_ERR_ALIGNMENT;
-    const NormBackParams p = {dy, h, dh, weight, rstd, dx, static_cast<float*>(workspace),
+    const NormBackParams p = {dy, h, dh, weight, rstd, dx, static_cast<float*>(workspace), dweight,
                               reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + b.dot_off), rows, cols, lddy,
                               ldh, lddh, lddx, wt == FP8BS_F32};
     return xt == FP8BS_BF16 ? launch_norm_back<__nv_bfloat16>(d, b, p, dweight, stream)

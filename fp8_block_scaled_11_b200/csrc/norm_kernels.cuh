@@ -479,6 +479,7 @@ struct NormBackParams {
     const float* rstd;
     void* dx;
     float* part;                // [parts][cols] partial sums of dw
+    float* dw;                  // dw itself, where one cluster takes all rows
     float* dot;                 // [rows] mean(g n) (wide rows only)
     int64_t rows, cols, lddy, ldh, lddh, lddx;
     int w_f32;
@@ -491,7 +492,7 @@ struct NormBackParams {
 // the CTA's rows of sums are added at the end, in order, into row blockIdx.x of
 // `part`.  Two CTAs of 256 threads an SM hide each other's sums and barriers: one
 // of 512, over two rows at a time, took 247 us where two took 195.
-template <typename T, int VPT, int THREADS, bool WREG>
+template <typename T, int VPT, int THREADS, bool WREG, bool CLUSTER>
 __global__ void __launch_bounds__(THREADS, (VPT == 1 ? 1024 : 512) / THREADS) rmsnorm_back_kernel(const NormBackParams p, const RowRing g)
 {
     extern __shared__ __align__(128) uint8_t ring_raw[];
@@ -574,19 +575,32 @@ __global__ void __launch_bounds__(THREADS, (VPT == 1 ? 1024 : 512) / THREADS) rm
     // the ring is empty: its memory takes the rows of sums
     float* out = p.part + (int64_t)blockIdx.x * p.cols;
     float* sums = reinterpret_cast<float*>(ring_raw);
+    const bool direct = !CLUSTER && g.ty == 1;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (i * g.tx + x) * 8;
-        if (c < p.cols) store8(g.ty == 1 ? out + c : sums + (int64_t)y * p.cols + c, dw[i]);
+        if (c < p.cols) store8(direct ? out + c : sums + (int64_t)y * p.cols + c, dw[i]);
     }
-    if (g.ty > 1) {
+    if (direct) return;
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
+        float t = sums[c];
+        for (int i = 1; i < g.ty; ++i) t += sums[(int64_t)i * p.cols + c];
+        (CLUSTER ? sums : out)[c] = t;
+    }
+    if constexpr (CLUSTER) {
+        // few rows: the cluster's CTAs add each other's sums, in rank order, from shared memory
         __syncthreads();
-        for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
-            float t = sums[c];
-            for (int i = 1; i < g.ty; ++i) t += sums[(int64_t)i * p.cols + c];
-            out[c] = t;
+        cluster_sync_all();
+        const uint32_t n = gridDim.x;
+        for (int c = (int)(blockIdx.x * blockDim.x + threadIdx.x); c < p.cols; c += (int)(n * blockDim.x)) {
+            float t = 0.f;
+            for (uint32_t i = 0; i < n; ++i) t += lds_cluster(mapa_shared(v.base + 4u * (uint32_t)c, i));
+            p.dw[c] = t;
         }
+        __syncthreads();
+        cluster_sync_all();
     }
 }
 

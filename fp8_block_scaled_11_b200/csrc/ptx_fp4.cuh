@@ -107,6 +107,14 @@ __device__ __forceinline__ void cluster_wait()
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// A float of a cluster CTA's shared memory.
+__device__ __forceinline__ float lds_cluster(uint32_t cluster_addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
 // 16 bytes into a cluster CTA's shared memory, counted on an mbarrier of the
 // same CTA (both shared::cluster addresses).
 __device__ __forceinline__ void st_async_v4(uint32_t cluster_addr, const uint32_t* r, uint32_t cluster_bar)

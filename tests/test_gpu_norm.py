@@ -178,7 +178,7 @@ def check_backward(dy, h, w, rstd, dh, got):
 
 
 BACK = [(1, 16), (1, 8192), (2, 5120), (33, 144), (300, 1040), (1200, 256), (700, 8192), (2500, 2064), (5, 8208),
-        (260, 16400), (3000, 128), (700, 96), (100, 64)]
+        (260, 16400), (3000, 128), (700, 96), (100, 64), (5, 1024), (60, 496), (250, 208)]
 
 
 def back_inputs(rows, cols, dtype, seed, wdtype=None):
