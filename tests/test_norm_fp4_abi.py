@@ -145,3 +145,40 @@ def test_binding_refuses():
         ops.fp4_scaled_gemm(q.float(), q, s, s)
     with pytest.raises(ValueError):
         ops.fp8bs_rmsnorm_backward(x, x.float(), w, torch.ones(4))                       # dy's dtype
+
+
+def test_binding_refuses_other_arguments():
+    """What is no tensor, no number, on no GPU, or laid out otherwise raises; nothing is called."""
+    x, w = torch.zeros(4, 256, dtype=torch.bfloat16), torch.ones(256, dtype=torch.bfloat16)
+    q, s, _, rstd, _ = out = ops.rmsnorm_quant_buffers(x)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.fp8_rmsnorm_quant_1x128(x, w, out=out)
+    with pytest.raises(TypeError):
+        ops.fp8_rmsnorm_quant_1x128(x, [1.0] * 256, out=out)
+    with pytest.raises(TypeError):
+        ops.fp8_rmsnorm_quant_1x128(x, w, eps="small", out=out)
+    with pytest.raises(ValueError):
+        ops.fp8_rmsnorm_quant_1x128(x, w, out=(q, s.contiguous(), None, rstd, None))       # a row-major grid
+    with pytest.raises(ValueError):
+        ops.fp8_rmsnorm_quant_1x128(x, w, out=(q, s, None, rstd.double(), None))
+    with pytest.raises(ValueError):
+        ops.fp8_rmsnorm_quant_1x128(x, w, out=(q[:, :128], s, None, rstd, None))
+    with pytest.raises(ValueError):
+        ops.fp8_rmsnorm_quant_1x128(torch.zeros(256, dtype=torch.bfloat16), w)              # no matrix
+    with pytest.raises(ValueError):
+        ops.rmsnorm_quant_buffers(x, bits=6)
+    c, t = torch.zeros(4, 128, dtype=torch.uint8), ops.fp4_scale_tiles(4, 256, "cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.fp4_scaled_gemm(c, c, t, t)
+    with pytest.raises(ValueError):
+        ops.fp4_scaled_gemm(c, c, t, t, out=torch.zeros(4, 5, dtype=torch.bfloat16))
+    with pytest.raises(TypeError):
+        ops.fp4_scaled_gemm(c, c, t, t, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        ops.fp4_scaled_gemm(c, c, t, t[..., :2])
+    with pytest.raises(TypeError):
+        ops.fp4_dequant_1x32(c, t, out_dtype=torch.float64)
+    with pytest.raises(ValueError):
+        ops.fp8bs_rmsnorm_backward(x, x, w, rstd, out=(x.clone(), torch.zeros(128)))
+    with pytest.raises(TypeError):
+        ops._load_native().norm(8, 0, x)                                                    # too few arguments
