@@ -74,9 +74,9 @@ __device__ __forceinline__ int share_lane(int i)
 // FULL: rows and columns are multiples of 128, nothing is tested.
 // --------------------------------------------------------------------------
 template <typename T, bool FULL>
-__global__ void __launch_bounds__(256) fp4_quant_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
-                                                             int64_t ldx, uint8_t* __restrict__ q, int64_t ldq,
-                                                             uint8_t* __restrict__ sf, int kcs)
+__global__ void __launch_bounds__(256) fp4_quant_rows_kernel(const T* x, int64_t rows, int64_t cols,
+                                                             int64_t ldx, uint8_t* q, int64_t ldq,
+                                                             uint8_t* sf, int kcs)
 {
     const int lane = threadIdx.x & 31;
     const int hw = threadIdx.x >> 4;
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(256) fp4_quant_rows_kernel(const T* __restrict
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (!FULL) v[i][j].zero();
-            if (row_ok(i, j)) v[i][j].load(src + (16 * i + 32 * j) * ldx);
+            if (row_ok(i, j)) load_stream(v[i][j], src + (16 * i + 32 * j) * ldx);
         }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -180,9 +180,9 @@ __device__ __forceinline__ void col_scale_bytes(const Block8x8<float>& b, uint32
 }
 
 template <typename T, bool FULL>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) fp4_quant_cols_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
-                                                             int64_t ldx, uint8_t* __restrict__ q, int64_t ldq,
-                                                             uint8_t* __restrict__ sf, int kcs, int tiles_c)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) fp4_quant_cols_kernel(const T* x, int64_t rows, int64_t cols,
+                                                             int64_t ldx, uint8_t* q, int64_t ldq,
+                                                             uint8_t* sf, int kcs, int tiles_c)
 {
     __shared__ __align__(16) uint8_t s_q[kQ4Cols * 128];
     __shared__ __align__(16) uint8_t s_sf[kQ4Cols * 8];
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) fp4_quant_cols_ke
 #pragma unroll
     for (int i = 0; i < 8; ++i, src += ldx) {
         if (!FULL) b.row[i].zero();
-        if (ok) b.row[i].load(src);
+        if (ok) load_stream(b.row[i], src);
     }
     uint32_t bytes[8];
     col_scale_bytes(b, bytes, threadIdx.x & 31);
@@ -241,9 +241,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) fp4_quant_cols_ke
 // fp4_quant_rows_kernel: a CTA owns a scale tile.
 // --------------------------------------------------------------------------
 template <typename T, bool FULL>
-__global__ void __launch_bounds__(256) fp4_dequant_kernel(const uint8_t* __restrict__ q, int64_t ldq,
-                                                          const uint8_t* __restrict__ sf, int64_t rows, int64_t cols,
-                                                          int kcs, T* __restrict__ out, int64_t ldo)
+__global__ void __launch_bounds__(256) fp4_dequant_kernel(const uint8_t* q, int64_t ldq,
+                                                          const uint8_t* sf, int64_t rows, int64_t cols,
+                                                          int kcs, T* out, int64_t ldo)
 {
     const int hw = threadIdx.x >> 4;
     const int rb = (int)blockIdx.x / kcs, kc = (int)blockIdx.x - rb * kcs;
@@ -265,10 +265,10 @@ __global__ void __launch_bounds__(256) fp4_dequant_kernel(const uint8_t* __restr
         const int dr = 16 * (i & 1) + 32 * (i >> 1);
         if (FULL || r0 + dr < rows) {
             if constexpr (kWide) {
-                const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src + dr * ldq));
+                const uint2 v = ld_stream_u2(src + dr * ldq);
                 w[i] = __byte_perm(v.x, v.y, odd ? 0x7632 : 0x5410);
             } else {
-                w[i] = __ldcs(reinterpret_cast<const uint32_t*>(src + dr * ldq));
+                w[i] = ld_stream_u1(src + dr * ldq);
             }
             byte[i] = scales[256 * (i & 1) + 4 * (i >> 1)];
         }

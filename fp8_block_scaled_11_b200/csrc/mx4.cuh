@@ -59,6 +59,24 @@ struct Eight {
     float2 v[4];
 };
 
+// Eight values read once, or (a norm's weight) again and again.
+__device__ __forceinline__ float4 as_float4(uint4 v)
+{
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ void load_stream(Vec8<__nv_bfloat16>& v, const __nv_bfloat16* p) { v.raw = ld_stream_u4(p); }
+__device__ __forceinline__ void load_stream(Vec8<float>& v, const float* p)
+{
+    v.a = as_float4(ld_stream_u4(p));
+    v.b = as_float4(ld_stream_u4(p + 4));
+}
+__device__ __forceinline__ void load_kept(Vec8<__nv_bfloat16>& v, const __nv_bfloat16* p) { v.raw = ld_u4(p); }
+__device__ __forceinline__ void load_kept(Vec8<float>& v, const float* p)
+{
+    v.a = as_float4(ld_u4(p));
+    v.b = as_float4(ld_u4(p + 4));
+}
+
 template <typename T>
 __device__ __forceinline__ Eight eight_of(const Vec8<T>& a)
 {

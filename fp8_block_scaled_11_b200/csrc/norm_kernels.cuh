@@ -82,27 +82,16 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const Eight& e)
                                               cvt_bf16x2(e.v[2].x, e.v[2].y), cvt_bf16x2(e.v[3].x, e.v[3].y));
 }
 
-// Eight weights (read-only, reused by every row).
-__device__ __forceinline__ void load_ro(Vec8<__nv_bfloat16>& v, const __nv_bfloat16* p)
-{
-    v.raw = __ldg(reinterpret_cast<const uint4*>(p));
-}
-__device__ __forceinline__ void load_ro(Vec8<float>& v, const float* p)
-{
-    v.a = __ldg(reinterpret_cast<const float4*>(p));
-    v.b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-}
-
 // Eight weights as fp32 (bf16 or fp32 in memory).
 __device__ __forceinline__ Eight load_weight8(const void* w, int w_f32, int64_t c)
 {
     if (w_f32) {
         Vec8<float> v;
-        load_ro(v, static_cast<const float*>(w) + c);
+        load_kept(v, static_cast<const float*>(w) + c);
         return eight_of(v);
     }
     Vec8<__nv_bfloat16> v;
-    load_ro(v, static_cast<const __nv_bfloat16*>(w) + c);
+    load_kept(v, static_cast<const __nv_bfloat16*>(w) + c);
     return eight_of(v);
 }
 
@@ -232,6 +221,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_quant_kernel(co
     const bool row_ok = FULL || r < p.rows;
     auto inside = [&](int c) { return FULL || (row_ok && c < p.cols); };
     Vec8<T> a[VPT];
+    Vec8<W> w0;
     float ss = 0.f;
     grid_begin();
     {
@@ -240,7 +230,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_quant_kernel(co
         for (int i = 0; i < VPT; ++i) {
             const int c = (i * tx + x) * 8;
             if (!FULL) a[i].zero();
-            if (inside(c)) a[i].load(src + c);
+            if (inside(c)) load_stream(a[i], src + c);
         }
     }
     if (p.res != nullptr) {
@@ -251,7 +241,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_quant_kernel(co
         for (int i = 0; i < VPT; ++i) {
             const int c = (i * tx + x) * 8;
             if (!FULL) b[i].zero();
-            if (inside(c)) b[i].load(res + c);
+            if (inside(c)) load_stream(b[i], res + c);
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -263,16 +253,21 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_quant_kernel(co
 #pragma unroll
     for (int i = 0; i < VPT; ++i) ss = sum_squares(eight_of(a[i]), ss);
     ss = row_sum(ss);
+    if constexpr (VPT == 1) {
+        w0.zero();
+        if (inside(x * 8)) load_kept(w0, static_cast<const W*>(p.w) + x * 8);
+    }
     const float rstd = rstd_of(ss, p.inv_cols, p.eps);
     if (row_ok && x == 0 && p.rstd != nullptr) p.rstd[r] = rstd;
     Eight y[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (i * tx + x) * 8;
-        Vec8<W> w;
-        if (!FULL) w.zero();
-        if (inside(c)) load_ro(w, static_cast<const W*>(p.w) + c);
-        y[i] = normalise(eight_of(a[i]), rstd, eight_of(w));
+        if constexpr (VPT > 1) {
+            if (!FULL) w0.zero();
+            if (inside(c)) load_kept(w0, static_cast<const W*>(p.w) + c);
+        }
+        y[i] = normalise(eight_of(a[i]), rstd, eight_of(w0));
     }
     if (p.y != nullptr) {
         T* dst = static_cast<T*>(p.y) + r * p.ldy;
@@ -440,10 +435,10 @@ __global__ void __launch_bounds__(512) rmsnorm_quant_wide_kernel(const NormParam
     grid_begin();
     for (int64_t c = (int64_t)threadIdx.x * 8; c < p.cols; c += (int64_t)blockDim.x * 8) {
         Vec8<T> a;
-        a.load(x + c);
+        load_stream(a, x + c);
         if (p.res != nullptr) {
             Vec8<T> b;
-            b.load(res + c);
+            load_stream(b, res + c);
             add_round(a, b);
             store_vec(h + c, a);
         }
@@ -460,7 +455,7 @@ __global__ void __launch_bounds__(512) rmsnorm_quant_wide_kernel(const NormParam
         Eight y[1] = {eight_zero()};
         if (c < p.cols) {
             Vec8<T> a;
-            a.load(src + c);
+            load_stream(a, src + c);
             y[0] = normalise(eight_of(a), rstd, load_weight8(p.w, p.w_f32, c));
             if (p.y != nullptr) store8(static_cast<T*>(p.y) + r * p.ldy + c, y[0]);
         }
@@ -509,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, (VPT == 1 ? 1024 : 512) / THREADS) rm
         for (int i = 0; i < VPT; ++i) {
             const int c = (i * g.tx + x) * 8;
             wr[i].zero();
-            if (c < p.cols) wr[i].load(static_cast<const T*>(p.w) + c);
+            if (c < p.cols) load_stream(wr[i], static_cast<const T*>(p.w) + c);
         }
     }
     auto weight = [&](int i, int c) {
@@ -521,13 +516,13 @@ __global__ void __launch_bounds__(THREADS, (VPT == 1 ? 1024 : 512) / THREADS) rm
     uint32_t phase = 0;
     // a row's rstd is loaded a block ahead
     const int64_t r_first = (int64_t)blockIdx.x * g.ty + y;
-    float rstd_next = r_first < p.rows ? __ldg(p.rstd + r_first) : 0.f;
+    float rstd_next = r_first < p.rows ? ld_f1(p.rstd + r_first) : 0.f;
     for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x, flip ^= 1) {
         const int64_t r = b * g.ty + y;
         const bool row_ok = r < p.rows;
         const float rstd = rstd_next;
         const int64_t r_next = r + (int64_t)gridDim.x * g.ty;
-        rstd_next = r_next < p.rows ? __ldg(p.rstd + r_next) : 0.f;
+        rstd_next = r_next < p.rows ? ld_f1(p.rstd + r_next) : 0.f;
         ring_wait(g, v, v.full(s), phase);
         const uint32_t at = v.base + (uint32_t)s * v.slot_bytes + (uint32_t)y * g.row_bytes;
         // n = h rstd:  dw += dy n,  dot = sum dy w h
@@ -613,8 +608,8 @@ __global__ void __launch_bounds__(512) rmsnorm_back_dot_kernel(const NormBackPar
     grid_begin();
     for (int64_t c = (int64_t)threadIdx.x * 8; c < p.cols; c += (int64_t)blockDim.x * 8) {
         Vec8<T> a, b;
-        a.load(static_cast<const T*>(p.dy) + r * p.lddy + c);
-        b.load(static_cast<const T*>(p.h) + r * p.ldh + c);
+        load_stream(a, static_cast<const T*>(p.dy) + r * p.lddy + c);
+        load_stream(b, static_cast<const T*>(p.h) + r * p.ldh + c);
         const Eight dy = eight_of(a), h = eight_of(b), w = load_weight8(p.w, p.w_f32, c);
 #pragma unroll
         for (int j = 0; j < 4; ++j) dot2 = ffma2(fmul2(dy.v[j], h.v[j]), w.v[j], dot2);
@@ -638,10 +633,10 @@ __global__ void __launch_bounds__(256) rmsnorm_back_wide_kernel(const NormBackPa
         const float rstd = p.rstd[r], k = -(rstd * rstd) * p.dot[r];
         const float2 rstd2 = make_float2(rstd, rstd), k2 = make_float2(k, k);
         Vec8<T> a, b, d;
-        a.load(static_cast<const T*>(p.dy) + r * p.lddy + c);
-        b.load(static_cast<const T*>(p.h) + r * p.ldh + c);
+        load_stream(a, static_cast<const T*>(p.dy) + r * p.lddy + c);
+        load_stream(b, static_cast<const T*>(p.h) + r * p.ldh + c);
         d.zero();
-        if (p.dh != nullptr) d.load(static_cast<const T*>(p.dh) + r * p.lddh + c);
+        if (p.dh != nullptr) load_stream(d, static_cast<const T*>(p.dh) + r * p.lddh + c);
         const Eight dy = eight_of(a), h = eight_of(b);
         Eight f = eight_of(d);
 #pragma unroll
@@ -659,8 +654,8 @@ __global__ void __launch_bounds__(256) rmsnorm_back_wide_kernel(const NormBackPa
 // warps' sums are added in a tree.
 constexpr int kDwWarps = 32;
 
-__global__ void __launch_bounds__(32 * kDwWarps) rmsnorm_dw_kernel(const float* __restrict__ part, int parts, int64_t cols,
-                                                                   float* __restrict__ dw)
+__global__ void __launch_bounds__(32 * kDwWarps) rmsnorm_dw_kernel(const float* part, int parts, int64_t cols,
+                                                                   float* dw)
 {
     __shared__ float s[kDwWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -672,7 +667,7 @@ __global__ void __launch_bounds__(32 * kDwWarps) rmsnorm_dw_kernel(const float* 
             float v[10];
 #pragma unroll
             for (int j = 0; j < 10; ++j)
-                v[j] = i + kDwWarps * j < parts ? __ldcg(part + (int64_t)(i + kDwWarps * j) * cols + c) : 0.f;
+                v[j] = i + kDwWarps * j < parts ? ld_l2_f1(part + (int64_t)(i + kDwWarps * j) * cols + c) : 0.f;
 #pragma unroll
             for (int j = 0; j < 10; ++j) sum += v[j];
         }

@@ -24,9 +24,9 @@ namespace fp8bs {
 constexpr int kReduceThreads = 128;
 constexpr int kReduceBatch = 16;         // split loads in flight per thread
 
-__global__ void __launch_bounds__(kReduceThreads) splitk_reduce_kernel(const float* __restrict__ ws, int splits,
+__global__ void __launch_bounds__(kReduceThreads) splitk_reduce_kernel(const float* ws, int splits,
                                                                        int64_t M, int64_t N, int64_t ldw,
-                                                                       void* __restrict__ D, int64_t ldd, int out_f32,
+                                                                       void* D, int64_t ldd, int out_f32,
                                                                        int vec_out)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -37,19 +37,19 @@ __global__ void __launch_bounds__(kReduceThreads) splitk_reduce_kernel(const flo
         const int64_t m = i / nq;
         const int64_t n = (i - m * nq) << 2;
         const float* src = ws + m * ldw + n;
-        float4 s = __ldcg(reinterpret_cast<const float4*>(src));
+        float4 s = ld_l2_f4(src);
         int k = 1;
         for (; k + kReduceBatch <= splits; k += kReduceBatch) {
             float4 v[kReduceBatch];
 #pragma unroll
-            for (int j = 0; j < kReduceBatch; ++j) v[j] = __ldcg(reinterpret_cast<const float4*>(src + (k + j) * plane));
+            for (int j = 0; j < kReduceBatch; ++j) v[j] = ld_l2_f4(src + (k + j) * plane);
 #pragma unroll
             for (int j = 0; j < kReduceBatch; ++j) {
                 s.x += v[j].x; s.y += v[j].y; s.z += v[j].z; s.w += v[j].w;
             }
         }
         for (; k < splits; ++k) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + k * plane));
+            const float4 v = ld_l2_f4(src + k * plane);
             s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
         }
         const float v[4] = {s.x, s.y, s.z, s.w};
