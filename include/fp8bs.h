@@ -440,9 +440,13 @@ fp8bs_status fp8_scaled_gemm_grouped(int64_t groups, const int64_t* group_rows, 
  * x, residual, weight, h, y, q and the scales 16-byte aligned, rstd 4-byte;
  * leading dims in bytes multiples of 16; ld_scale % 4 == 0.  eps >= 0; eps = 0
  * with an all-zero row divides by zero.  Inputs must be finite, and a row's sum
- * of squares and its y must fit fp32: a row where they are not has a NaN rstd, and
- * NaN in all its e4m3 codes or 4-bit scales.  Other than h, no output may overlap an
- * input or another output.  Errors as the quantizations.
+ * of squares and its y must fit fp32.  A row with an input that is not finite, or
+ * whose sum of squares does not fit, has a NaN rstd, and NaN in all its e4m3 codes
+ * or 4-bit scales.  Where only a value of y does not fit (a weight near the type's
+ * limit), rstd is as ever, and that value's group alone is NaN once its scale is
+ * applied: scale_inv is infinite over codes of 0 and NaN (8 bits), or the scale is
+ * the NaN byte 255 (4 bits).  Other than h, no output may overlap an input or
+ * another output.  Errors as the quantizations.
  */
 fp8bs_status fp8_rmsnorm_quant_1x128(const void* x, int64_t ldx, const void* residual, int64_t ld_res, fp8bs_dtype xt,
                                      int64_t rows, int64_t cols, const void* weight, fp8bs_dtype wt, float eps,
