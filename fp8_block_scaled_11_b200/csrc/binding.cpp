@@ -306,11 +306,30 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
-// (M, N, K) -> bytes
+// Makes the CUDA device of that index current, as the calls do (-1: none does).
+void make_current(c10::cuda::OptionalCUDAGuard& guard, PyObject* index)
+{
+    const long i = integer(index, "device");
+    if (i >= 0) guard.set_index((c10::DeviceIndex)i);
+}
+
+// (M, N, K, device) -> bytes
 PyObject* product_workspace(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return guarded(n, 3, [&] {
+    return guarded(n, 4, [&] {
+        c10::cuda::OptionalCUDAGuard guard;
+        make_current(guard, a[3]);
         return PyLong_FromSize_t(fp4_scaled_gemm_workspace_size(integer(a[0], "M"), integer(a[1], "N"), integer(a[2], "K")));
+    });
+}
+
+// (rows, cols, device) -> bytes
+PyObject* norm_backward_workspace(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded(n, 3, [&] {
+        c10::cuda::OptionalCUDAGuard guard;
+        make_current(guard, a[2]);
+        return PyLong_FromSize_t(fp8bs_rmsnorm_backward_workspace_size(integer(a[0], "rows"), integer(a[1], "cols")));
     });
 }
 
@@ -326,7 +345,8 @@ PyMODINIT_FUNC PyInit__binding()
 {
     static PyMethodDef methods[] = {method("norm", norm), method("norm_backward", norm_backward), method("quant", quant),
                                     method("dequant", dequant), method("product", product),
-                                    method("product_workspace", product_workspace), {nullptr, nullptr, 0, nullptr}};
+                                    method("product_workspace", product_workspace),
+                                    method("norm_backward_workspace", norm_backward_workspace), {nullptr, nullptr, 0, nullptr}};
     static PyModuleDef def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
     return PyModule_Create(&def);
 }

@@ -415,6 +415,13 @@ def _load_native():
     return _native
 
 
+def _index(device) -> int:
+    """The index of a CUDA device (-1: the current one, or no CUDA device): a workspace is sized for the device it is
+    allocated on."""
+    d = device if isinstance(device, torch.device) else torch.device(device)
+    return d.index if d.type == "cuda" and d.index is not None else -1
+
+
 # ---------------------------------------------------------------------------- microscaled 4 bits
 def fp4_scale_tiles(rows: int, cols: int, device) -> torch.Tensor:
     """Allocate the scale tiles of a rows x cols matrix of 4-bit codes: a uint8
@@ -459,7 +466,7 @@ def fp4_dequant_1x32(q: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dtyp
 
 def fp4_scaled_gemm_workspace(M: int, N: int, K: int, device) -> Optional[torch.Tensor]:
     """Allocate the split-K workspace of a product of these sizes (None where it needs none)."""
-    n = (_native or _load_native()).product_workspace(M, N, K)
+    n = (_native or _load_native()).product_workspace(M, N, K, _index(device))
     return torch.empty((n,), dtype=torch.uint8, device=device) if n else None
 
 
@@ -531,7 +538,7 @@ def fp4_rmsnorm_quant_1x32(x: torch.Tensor, weight: torch.Tensor, residual: Opti
 
 def rmsnorm_backward_workspace(h: torch.Tensor) -> torch.Tensor:
     """Allocate the workspace of fp8bs_rmsnorm_backward for inputs like h."""
-    n = int(lib().fp8bs_rmsnorm_backward_workspace_size(h.shape[0], h.shape[1]))
+    n = (_native or _load_native()).norm_backward_workspace(h.shape[0], h.shape[1], _index(h.device))
     return torch.empty((n,), dtype=torch.uint8, device=h.device)
 
 
