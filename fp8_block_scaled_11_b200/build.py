@@ -1,10 +1,13 @@
-"""Build step, in-tree: the CUDA library (csrc/fp8bs_lib.cu -> libfp8bs.so) and
-the extension module over it that ops.py calls for the norm and the 4-bit
-operators (csrc/binding.cpp -> _binding.so).
+"""Build step, in-tree: the CUDA library (csrc/fp8bs_lib.cu -> libfp8bs.so, with
+nvcc alone) and, where torch is installed, the extension module over it that
+ops.py calls for the norm and the 4-bit operators (csrc/binding.cpp ->
+_binding.<Python's ABI>.torch-<version>.so).  The module's name holds what it was
+built for: after another torch or Python is installed it is built again.
 
 The library is compiled for sm_100a only (B200), no fast-math: the
 quantization's fp32 division and reciprocal must be IEEE round-to-nearest.
 """
+import importlib.metadata
 import importlib.util
 import os
 import subprocess
@@ -18,7 +21,6 @@ MAIN = os.path.join(SRC_DIR, "fp8bs_lib.cu")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(HERE, "libfp8bs.so")
 BINDING = os.path.join(SRC_DIR, "binding.cpp")
-BINDING_PATH = os.path.join(HERE, "_binding.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -54,14 +56,18 @@ def _run(cmd, path: str):
     os.replace(tmp, path)
 
 
-def _build_binding():
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+def binding_path() -> str:
+    """The extension module for this Python and the installed torch."""
+    return os.path.join(HERE, f"_binding.{sysconfig.get_config_var('SOABI')}.torch-{importlib.metadata.version('torch')}.so")
+
+
+def _build_binding(torch: str):
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"),
           "-isystem", os.path.join(cuda, "include"), BINDING, "-L", HERE, "-l:libfp8bs.so",
           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
-          "-Wl,-rpath,$ORIGIN"], BINDING_PATH)
+          "-Wl,-rpath,$ORIGIN"], binding_path())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -70,8 +76,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         _run(cmd, LIB_PATH)
-    if force or _older(BINDING_PATH, [BINDING, os.path.join(INCLUDE, "fp8bs.h")]):
-        _build_binding()
+    torch = importlib.util.find_spec("torch")
+    if torch is not None and (force or _older(binding_path(), [BINDING, os.path.join(INCLUDE, "fp8bs.h")])):
+        _build_binding(torch.submodule_search_locations[0])
     return LIB_PATH
 
 

@@ -13,6 +13,7 @@ torch they are returned as (rows, groups) views with strides (1, ld): element
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
@@ -408,10 +409,13 @@ def _load_native():
     """The extension module that checks the arguments of the functions below and calls the library (csrc/binding.cpp)."""
     global _native
     lib()
-    if not os.path.exists(_build.BINDING_PATH):
-        raise ImportError(f"_binding.so not built ({_build.BINDING_PATH}); run fp8_block_scaled_11_b200/build.py")
-    from . import _binding
-    _native = _binding
+    path = _build.binding_path()
+    if not os.path.exists(path):
+        raise ImportError(f"the extension module is not built ({path}); run fp8_block_scaled_11_b200/build.py")
+    spec = importlib.util.spec_from_file_location(f"{__package__}._binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    _native = module
     return _native
 
 
