@@ -26,6 +26,7 @@
 #include "fp4_quant_kernels.cuh"
 #include "gemm_fp4_kernel.cuh"
 #include "gemm_fp4_pair_kernel.cuh"
+#include "norm_fp4_plan.cuh"
 
 using namespace fp8bs;
 
@@ -52,7 +53,7 @@ struct DeviceInfo {
     std::atomic<bool> ring_attr_set[32]{};   // RMS norm backward, per instantiation
     std::atomic<bool> fp4_attr_set[4]{};     // 4-bit product on single CTAs, per tile width
     std::atomic<int> fp4_clusters[4][4]{};   // and co-resident clusters of 2^i CTAs
-    std::atomic<int> fp4_pair_clusters{};    // 4-bit product on CTA pairs: co-resident pairs
+    std::atomic<int> fp4_pair_clusters{};    // 4-bit product on CTA pairs: co-resident pairs (-1: none)
 };
 
 DeviceInfo g_dev[kMaxDevices];
@@ -99,7 +100,6 @@ fp8bs_status get_device(DeviceInfo** out)
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t dtype_size(fp8bs_dtype t) { return t == FP8BS_F32 ? 4 : 2; }
 inline bool valid_dtype(fp8bs_dtype t) { return t == FP8BS_BF16 || t == FP8BS_F32; }
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 fp8bs_status launch_status()
 {

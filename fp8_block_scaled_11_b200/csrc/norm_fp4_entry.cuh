@@ -249,84 +249,6 @@ fp8bs_status launch_norm_back(DeviceInfo* d, const BackPlan& b, const NormBackPa
 }
 
 // ---------------------------------------------------------------- 4-bit product
-struct Fp4Plan {
-    bool pair;                  // 256 x 256 tiles on CTA pairs; else 128 x bn tiles on single CTAs
-    int bn;
-    int tiles_m, tiles_n;
-    int parts;                  // CTAs of a cluster that share a tile's K
-    int splits;                 // parts of K that go through the workspace
-    int64_t ldw;
-    size_t ws_bytes;
-};
-
-// What a product takes on single CTAs, in us: units (a tile's part of K) over SMs
-// that hold two, each round of them the tile's fixed part and its steps of 256 K,
-// where a round leaves an SM to each unit (`fixed`, `step`) or puts two on it
-// (`fixed2`, `step2`), and what sending and adding a cluster's sums adds.
-struct Fp4Cost {
-    double fixed, step, fixed2, step2, send, send2;
-};
-
-double fp4_single_us(const Fp4Cost& c, int64_t units, int64_t steps, bool send, int num_sms)
-{
-    const int64_t room = 2 * num_sms, rounds = units / room, rest = units % room;
-    double us = (double)rounds * (c.fixed2 + c.step2 * (double)steps);
-    if (rest > num_sms) us += c.fixed2 + c.step2 * (double)steps;
-    else if (rest > 0) us += c.fixed + c.step * (double)steps;
-    return us + (!send ? 0. : units > num_sms ? c.send2 : c.send);
-}
-
-// Tiles and the split of K: the fastest of CTA pairs and of single CTAs with each
-// tile width and cluster size, by models of their times fitted to 600 measured
-// ones (M 130 .. 4096, N 1000 .. 32000, K 256 .. 8192), where the choice costs
-// 0.6% over the fastest in the mean and 14% at most.  Measured: 1024 x 5120 x 8192
-// 24.7 us on pairs, 31.5 on single CTAs of 128 columns; 512 x 8192 x 256 4.6 with
-// 128 columns, 7.4 with 64; 256 x 2080 x 8192 10.3 with 64 columns over clusters of
-// four, 13.6 on pairs; 72 x 5120 x 8192 9.0 over clusters of four, 14.2 without.
-Fp4Plan plan_fp4(int64_t M, int64_t N, int64_t K, int num_sms)
-{
-    static constexpr Fp4Cost kCost[4] = {{0.2, 0.30, 0.2, 0.30, 0.35, 0.5},       // 16 columns
-                                         {0.4, 0.30, 0.4, 0.30, 0.7, 1.0},        // 32
-                                         {2.1, 0.38, 2.8, 0.41, 1.3, 1.8},        // 64
-                                         {2.5, 0.39, 3.3, 0.45, 2.6, 3.2}};       // 128
-    Fp4Plan s = {};
-    const int64_t steps = cdiv(K, kF4StepK);
-    s.tiles_n = (int)cdiv(N, kF4Rows);
-    s.parts = 1;
-    s.splits = 1;
-    double best = 1e30;
-    // the narrowest tile that holds every token, or either of the two widest ones
-    for (int i = M <= 16 ? 0 : M <= 32 ? 1 : 2, bn = 16 << i; i < 4; ++i, bn *= 2) {
-        const int64_t units = cdiv(M, bn) * s.tiles_n;
-        for (int parts = 1; parts <= kF4MaxCluster; parts *= 2) {
-            if (parts > 1 && (units * parts > 2 * num_sms || steps < 2 * parts)) break;
-            const double us = fp4_single_us(kCost[i], units * parts, cdiv(steps, parts), parts > 1, num_sms);
-            if (us < best) {
-                best = us;
-                s.bn = bn;
-                s.parts = parts;
-            }
-        }
-        if (M <= bn) break;
-    }
-    const int64_t waves = cdiv(cdiv(M, kF4Pair) * cdiv(N, kF4Pair), std::max(1, num_sms / 2));
-    s.pair = M > 128 && 2.85 + (double)waves * (1.48 + 0.308 * (double)steps) < best;
-    if (s.pair) {
-        s.bn = kF4Pair;
-        s.tiles_n = (int)cdiv(N, kF4Pair);
-        s.parts = 1;
-    } else {
-        // very long K over clusters too, where they leave half of the room and 8 steps a CTA
-        const int64_t ctas = cdiv(M, s.bn) * s.tiles_n * s.parts;
-        if (s.parts == kF4MaxCluster)
-            s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({2 * num_sms / ctas, steps / (8 * s.parts), 32}));
-    }
-    s.tiles_m = (int)cdiv(M, s.bn);
-    s.ldw = (N + 3) & ~int64_t(3);
-    s.ws_bytes = s.splits > 1 ? (size_t)s.splits * (size_t)M * (size_t)s.ldw * sizeof(float) : 0;
-    return s;
-}
-
 template <int BN>
 fp8bs_status launch_fp4(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap& tT, const Fp4Params& p, int parts,
                         cudaStream_t stream)
@@ -382,7 +304,43 @@ fp8bs_status launch_fp4(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap&
     return launch_status();
 }
 
-fp8bs_status launch_fp4_pair(DeviceInfo* d, const CUtensorMap& tW, const CUtensorMap& tT, const Fp4Params& p,
+// The pair kernel's attributes, once per device: the pairs that can be resident at
+// once, or none where it cannot run as built.
+constexpr int kNoPairs = -1;
+
+fp8bs_status fp4_pairs(DeviceInfo* d, int* pairs)
+{
+    *pairs = d->fp4_pair_clusters.load(std::memory_order_acquire);
+    if (*pairs != 0) return FP8BS_OK;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    *pairs = d->fp4_pair_clusters.load(std::memory_order_relaxed);
+    if (*pairs != 0) return FP8BS_OK;
+    auto k = gemm_fp4_pair_kernel;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Fp4PairSmem::alloc) != cudaSuccess)
+        return FP8BS_ERR_CUDA;
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, k) != cudaSuccess) return FP8BS_ERR_CUDA;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * std::max(1, d->num_sms / 2), 1, 1);
+    cfg.blockDim = dim3(kF4PairThreads, 1, 1);
+    cfg.dynamicSmemBytes = Fp4PairSmem::alloc;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int nc = 0;
+    if (cudaOccupancyMaxActiveClusters(&nc, k, &cfg) != cudaSuccess) return FP8BS_ERR_CUDA;
+    // the register hand-over is sized for this exact allocation at launch: with fewer
+    // the epilogue's increase could never be granted
+    *pairs = fa.numRegs == kF4LaunchRegs && nc > 0 ? nc : kNoPairs;
+    d->fp4_pair_clusters.store(*pairs, std::memory_order_release);
+    return FP8BS_OK;
+}
+
+fp8bs_status launch_fp4_pair(int pairs, const CUtensorMap& tW, const CUtensorMap& tT, const Fp4Params& p,
                              cudaStream_t stream)
 {
     // scale tiles as rows of 128-row blocks of 64-bit words: four tiles (2048
@@ -394,43 +352,8 @@ fp8bs_status launch_fp4_pair(DeviceInfo* d, const CUtensorMap& tW, const CUtenso
         st = make_map(&tST, CU_TENSOR_MAP_DATA_TYPE_INT64, 8, p.sfa, (uint64_t)p.kcs * 64, cdiv(p.M, 128),
                       (uint64_t)p.kcs * kSfTileBytes, 256, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (st != FP8BS_OK) return st;
-    auto k = gemm_fp4_pair_kernel;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kF4PairThreads, 1, 1);
-    cfg.dynamicSmemBytes = Fp4PairSmem::alloc;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int nc = d->fp4_pair_clusters.load(std::memory_order_acquire);
-    if (nc == 0) {
-        std::lock_guard<std::mutex> lock(g_mutex);
-        nc = d->fp4_pair_clusters.load(std::memory_order_relaxed);
-        if (nc == 0) {
-            if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Fp4PairSmem::alloc) !=
-                cudaSuccess)
-                return FP8BS_ERR_CUDA;
-            // the register hand-over is sized for this exact allocation at launch:
-            // with fewer the epilogue's increase could never be granted
-            cudaFuncAttributes fa;
-            if (cudaFuncGetAttributes(&fa, k) != cudaSuccess) return FP8BS_ERR_CUDA;
-            if (fa.numRegs != kF4LaunchRegs) return FP8BS_ERR_UNSUPPORTED;
-            cfg.gridDim = dim3(2 * std::max(1, d->num_sms / 2), 1, 1);
-            if (cudaOccupancyMaxActiveClusters(&nc, k, &cfg) != cudaSuccess) return FP8BS_ERR_CUDA;
-            if (nc < 1) return FP8BS_ERR_UNSUPPORTED;
-            d->fp4_pair_clusters.store(nc, std::memory_order_release);
-        }
-    }
-    cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(p.num_units, nc)), 1, 1);
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, k, tW, tT, tSW, tST, p) != cudaSuccess) return FP8BS_ERR_CUDA;
-    return launch_status();
+    return launch_early_cluster(gemm_fp4_pair_kernel, (unsigned)(2 * std::min<int64_t>(p.num_units, pairs)),
+                                kF4PairThreads, Fp4PairSmem::alloc, stream, 2, tW, tT, tSW, tST, p);
 }
 
 // The split-K reduction, as a programmatic dependent of the product.
@@ -607,6 +530,14 @@ fp8bs_status fp4_scaled_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* A, 
     fp8bs_status st = get_device(&d);
     if (st != FP8BS_OK) return st;
     Fp4Plan plan = plan_fp4(M, N, K, d->num_sms);
+    int pairs = 0;
+    if (plan.pair) {
+        if ((st = fp4_pairs(d, &pairs)) != FP8BS_OK) return st;
+        if (pairs == kNoPairs) {
+            plan = plan_fp4(M, N, K, d->num_sms, false);
+            plan.splits = 1;                // (the caller was told that no workspace is needed)
+        }
+    }
     if (plan.splits > 1) {
         if (workspace == nullptr && workspace_bytes == 0) plan.splits = 1;      // split-K disabled by the caller
         else if (workspace == nullptr || workspace_bytes < plan.ws_bytes) return FP8BS_ERR_WORKSPACE;
@@ -645,7 +576,7 @@ fp8bs_status fp4_scaled_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* A, 
     p.ws = static_cast<float*>(workspace);
     p.ldw = plan.ldw;
     p.err = d->err_ptr;
-    if (plan.pair) return launch_fp4_pair(d, tW, tT, p, stream);
+    if (plan.pair) return launch_fp4_pair(pairs, tW, tT, p, stream);
     switch (plan.bn) {
     case 16: st = launch_fp4<16>(d, tW, tT, p, plan.parts, stream); break;
     case 32: st = launch_fp4<32>(d, tW, tT, p, plan.parts, stream); break;
