@@ -35,8 +35,6 @@ fp8bs_status launch_early(void (*k)(P...), dim3 grid, dim3 block, size_t smem, c
     return launch_early_cluster(k, grid, block, smem, stream, 1, args...);
 }
 
-inline int64_t round32(int64_t v) { return (v + 31) / 32 * 32; }
-
 // ---------------------------------------------------------------- RMS norm
 // The arguments both forward entry points share.
 fp8bs_status check_norm(const NormParams& p, fp8bs_dtype xt, fp8bs_dtype wt)
@@ -59,29 +57,6 @@ fp8bs_status check_norm(const NormParams& p, fp8bs_dtype xt, fp8bs_dtype wt)
     if (p.res != nullptr && ((p.ldr * e) % 16 || (p.ldh * e) % 16)) return FP8BS_ERR_ALIGNMENT;
     if (p.y != nullptr && (p.ldy * e) % 16) return FP8BS_ERR_ALIGNMENT;
     return FP8BS_OK;
-}
-
-// Threads per row (16, or a multiple of 32) and eights per thread for a row of
-// `eights` eights: the pair that leaves the fewest threads idle, at most max_tx
-// threads; among equals the first of `order`.
-struct RowShape {
-    int tx, vpt;                // vpt == 0: the row is too wide
-};
-
-inline int64_t round_row(int64_t tx) { return tx <= 16 ? 16 : round32(tx); }
-
-RowShape row_shape(int64_t eights, int64_t max_tx, const int (&order)[3])
-{
-    RowShape best = {0, 0};
-    int64_t best_idle = INT64_MAX;
-    for (int vpt : order) {
-        const int64_t tx = round_row(cdiv(eights, vpt));
-        if (tx <= max_tx && tx * vpt - eights < best_idle) {
-            best_idle = tx * vpt - eights;
-            best = {(int)tx, vpt};
-        }
-    }
-    return best;
 }
 
 template <typename T, typename W, int BITS>
@@ -112,73 +87,6 @@ fp8bs_status launch_norm(DeviceInfo* d, const NormParams& p, fp8bs_dtype xt, cud
                        : launch_norm_rows<__nv_bfloat16, __nv_bfloat16, BITS>(d, p, stream);
     return p.w_f32 ? launch_norm_rows<float, float, BITS>(d, p, stream)
                    : launch_norm_rows<float, __nv_bfloat16, BITS>(d, p, stream);
-}
-
-// The backward's launch and the bytes of its workspace.  Rows are read once, over
-// a ring, where two slots of one fit (up to 16384 columns of bf16, 8192 of fp32);
-// wider ones take two launches.
-struct BackPlan {
-    RowShape shape;             // vpt == 0: wide rows
-    int ty, slots, per_sm;      // rows per block of the ring, its depth, CTAs per SM
-    int cluster;                // CTAs of the one cluster that takes all rows (0: many CTAs, and a second launch)
-    uint32_t smem;
-    int64_t grid, parts;
-    size_t dot_off, bytes;
-};
-
-constexpr uint32_t kRingSmem = 222 * 1024;      // of an SM's shared memory
-constexpr int kBackCluster = 8;                 // CTAs of a cluster, at most
-
-BackPlan plan_back(int64_t rows, int64_t cols, int64_t elem, int mats, int num_sms)
-{
-    BackPlan b = {};
-    const int64_t eights = cdiv(cols, 8);
-    const uint32_t row_bytes = (uint32_t)std::min<int64_t>(cols * elem, kRingSmem);
-    // eights per thread: one where 16 threads hold a row (100000 x 128 bf16 21 us, with
-    // two 26), over 1024 threads of an SM; else four or two over 512, whichever keeps
-    // more of them at work.  Among equals four (16640 x 1616 bf16 39 us, with two 47),
-    // but two where the SMs have under three rows each, whose latency counts (161 x
-    // 3776 bf16 6.0 us, with four 6.2; 333 x 1040 fp32 5.8 and 6.4).  A CTA has 256
-    // threads (or one row's) and room for two slots.
-    double best = 0.;
-    for (int i = 0; i < 2; ++i) {
-        const bool narrow = eights <= 16;
-        const bool two_first = rows < 3 * num_sms && eights <= 512;     // (at most 256 threads a row)
-        const int vpt = narrow ? 1 : two_first == (i == 0) ? 2 : 4;
-        const int64_t tx = narrow ? 16 : round_row(cdiv(eights, vpt));
-        if (tx > 512) continue;
-        int ty = std::max(1, (int)(256 / tx));
-        while (ty > 1 && cdiv(rows, ty) < num_sms) ty /= 2;             // few rows: over more SMs
-        if (tx == 16) ty = (ty + 1) / 2 * 2;                            // whole warps
-        const uint32_t slot = ring_smem(row_bytes, ty, mats, 1);
-        const int per_sm = (int)std::min<int64_t>((narrow ? 1024 : 512) / (tx * ty), kRingSmem / (2 * slot + 1024));
-        const double busy = (double)per_sm * (double)ty * (double)eights / vpt;
-        if (per_sm < 1 || busy <= best) continue;
-        best = busy;
-        b.shape = {(int)tx, vpt};
-        b.ty = ty;
-        b.per_sm = per_sm;
-        b.slots = (int)std::min<uint32_t>(4, (kRingSmem / (uint32_t)per_sm - 1024) / slot);
-        b.smem = ring_smem(row_bytes, ty, mats, b.slots);
-    }
-    if (b.shape.vpt > 0) b.grid = std::min<int64_t>(cdiv(rows, b.ty), (int64_t)b.per_sm * num_sms);
-    else b.grid = std::max<int64_t>(1, std::min<int64_t>(rows, 8 * num_sms / cdiv(cols, 2048)));
-    b.parts = b.grid;
-    b.dot_off = (size_t)(b.parts * cols) * sizeof(float);
-    b.bytes = b.dot_off + (b.shape.vpt == 0 ? (size_t)((rows + 3) / 4 * 4) * sizeof(float) : 0);
-    // few narrow rows: one cluster takes them all and adds up dw itself, without the
-    // second launch (64 x 512 bf16 4.0 us instead of 4.3, called from Python 4.6
-    // instead of 6.2; 16 x 1024 4.5 and 4.1, 5.0 and 6.1; at 4096 columns slower)
-    const int ty = b.shape.vpt > 0 ? 256 / std::min(b.shape.tx, 256) : 1;
-    const int64_t blocks = cdiv(rows, ty);
-    if ((b.shape.vpt == 1 || b.shape.vpt == 2) && blocks <= (b.shape.tx == 16 ? 2 : b.shape.tx <= 64 ? 1 : 0) * kBackCluster) {
-        b.cluster = blocks > 4 ? kBackCluster : blocks > 2 ? 4 : (int)blocks;
-        b.ty = ty;
-        b.slots = 2;
-        b.smem = ring_smem(row_bytes, ty, mats, 2);
-        b.grid = b.cluster;
-    }
-    return b;
 }
 
 template <typename T, int VPT, int THREADS, bool WREG, bool CLUSTER = false>
