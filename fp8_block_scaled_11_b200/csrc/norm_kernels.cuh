@@ -253,20 +253,21 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_quant_kernel(co
 #pragma unroll
     for (int i = 0; i < VPT; ++i) ss = sum_squares(eight_of(a[i]), ss);
     ss = row_sum(ss);
-    if constexpr (VPT == 1) {
-        w0.zero();
-        if (inside(x * 8)) load_kept(w0, static_cast<const W*>(p.w) + x * 8);
-    }
+    // the first weights arrive during the reciprocal root, but not fp32 weights of bf16
+    // rows, whose registers cost a CTA an SM (16640 x 8192 without residual 85 -> 101 us)
+    constexpr bool kEarly = VPT == 1 || sizeof(W) <= sizeof(T);
+    auto weights = [&](int c) {
+        if (!FULL) w0.zero();
+        if (inside(c)) load_kept(w0, static_cast<const W*>(p.w) + c);
+    };
+    if (kEarly) weights(x * 8);
     const float rstd = rstd_of(ss, p.inv_cols, p.eps);
     if (row_ok && x == 0 && p.rstd != nullptr) p.rstd[r] = rstd;
     Eight y[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = (i * tx + x) * 8;
-        if constexpr (VPT > 1) {
-            if (!FULL) w0.zero();
-            if (inside(c)) load_kept(w0, static_cast<const W*>(p.w) + c);
-        }
+        if (!kEarly || i > 0) weights(c);
         y[i] = normalise(eight_of(a[i]), rstd, eight_of(w0));
     }
     if (p.y != nullptr) {
