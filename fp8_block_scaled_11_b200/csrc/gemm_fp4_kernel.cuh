@@ -13,7 +13,7 @@
 // consecutive elements of a row of D.
 //
 // The kernel of few tokens is bound by the weight's bytes and its own latency (one
-// token by 5120 x 8192: 5.4 us, of which 3.4 are the bytes at the measured copy
+// token by 5120 x 8192: 5.6 us, of which 3.4 are the bytes at the measured copy
 // rate; about 800 cycles of set-up, 800 to the first bytes, 500 a step of 20 KB,
 // 1300 from the last step to the accumulator, 900 for the sums).
 //

@@ -12,8 +12,8 @@
 // All sums are fp32, each in an order that the sizes and the device fix.  Both
 // passes are bound by memory: the forward reads x and the residual and writes h
 // and the codes once, the backward reads dy, h and dh and writes dx once.  At
-// 16640 x 8192 bf16 the forward with residual takes 144 us and the backward with
-// dh 172, 6.6 and 6.3 TB/s (a plain copy reaches 6.5).
+// 16640 x 8192 bf16 the forward with residual takes 144-147 us and the backward
+// with dh 171-175, 6.5-6.7 and 6.2-6.4 TB/s (a plain copy reaches 6.5).
 #pragma once
 
 #include <cstdint>
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_quant_kernel(co
 // waits for its sum.  Warp 0 refills a slot once every warp has arrived on its
 // empty barrier.  The backward pass uses it, whose CTAs must live long to keep
 // their sums of dw; the forward pass is faster with a CTA per row and many of them
-// on an SM (16640 x 8192 bf16 with residual: 148 us, over a ring 203).
+// on an SM (16640 x 8192 bf16 with residual: 144-147 us, over a ring 203).
 //
 // A wait that runs out (bounded as everywhere) raises the error flag and the
 // CTA's abort flag and goes on: the row's barriers stay matched and the kernel
