@@ -7,6 +7,7 @@ built for: after another torch or Python is installed it is built again.
 The library is compiled for sm_100a only (B200), no fast-math: the
 quantization's fp32 division and reciprocal must be IEEE round-to-nearest.
 """
+import importlib
 import importlib.metadata
 import importlib.util
 import os
@@ -58,7 +59,11 @@ def _run(cmd, path: str):
 
 def binding_path() -> str:
     """The extension module for this Python and the installed torch."""
-    return os.path.join(HERE, f"_binding.{sysconfig.get_config_var('SOABI')}.torch-{importlib.metadata.version('torch')}.so")
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = importlib.import_module("torch").__version__
+    return os.path.join(HERE, f"_binding.{sysconfig.get_config_var('SOABI')}.torch-{version}.so")
 
 
 def _build_binding(torch: str):

@@ -422,6 +422,8 @@ def _load_native():
 def _index(device) -> int:
     """The index of a CUDA device (-1: the current one, or no CUDA device): a workspace is sized for the device it is
     allocated on."""
+    if device is None:
+        return -1
     d = device if isinstance(device, torch.device) else torch.device(device)
     return d.index if d.type == "cuda" and d.index is not None else -1
 

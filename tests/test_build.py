@@ -27,6 +27,17 @@ def test_without_torch(made, monkeypatch):
     assert made == [("nvcc", build.LIB_PATH)]
 
 
+def test_torch_without_metadata(made, monkeypatch):
+    """A torch that was never installed by a package tool says its version itself."""
+    import torch
+
+    def none(name):
+        raise importlib.metadata.PackageNotFoundError(name)
+    monkeypatch.setattr(importlib.metadata, "version", none)
+    build.build(force=True)
+    assert torch.__version__ in made[1][1]
+
+
 def test_with_torch(made):
     build.build(force=True)
     assert [c for c, _ in made] == ["nvcc", "g++"] and made[0][1] == build.LIB_PATH

@@ -20,7 +20,8 @@ def asked(monkeypatch):
     return calls
 
 
-@pytest.mark.parametrize("device,index", [("cuda:1", 1), (torch.device("cuda", 3), 3), ("cuda", -1), ("cpu", -1), (2, 2)])
+@pytest.mark.parametrize("device,index", [("cuda:1", 1), (torch.device("cuda", 3), 3), ("cuda", -1), ("cpu", -1), (2, 2),
+                                          (None, -1)])
 def test_product(asked, device, index):
     assert ops.fp4_scaled_gemm_workspace(16, 130, 131072, device) is None
     assert asked == [("product", (16, 130, 131072, index))]
