@@ -19,6 +19,7 @@
 #include <cstdint>
 #include <cuda_fp16.h>
 #include "ptx.cuh"
+#include "ptx_load.cuh"
 #include "quant_kernels.cuh"
 
 namespace fp8bs {

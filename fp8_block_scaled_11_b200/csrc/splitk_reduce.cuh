@@ -18,6 +18,7 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 #include "ptx.cuh"
+#include "ptx_load.cuh"
 
 namespace fp8bs {
 

@@ -6,7 +6,7 @@ lifetime.  The non-coherent path (__ldg, ld.global.nc, and what a compiler may m
 of a load through a pointer declared const and __restrict__) is defined only for
 memory that nobody writes while the kernel runs, and a load that promises so may be
 moved in front of griddepcontrol.wait.  Cache-hinted loads are the wrappers of
-ptx.cuh, which no compiler moves across that wait."""
+ptx_load.cuh, which no compiler moves across that wait."""
 import os
 import re
 
@@ -14,7 +14,7 @@ import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "fp8_block_scaled_11_b200", "csrc")
 FILES = ["norm_kernels.cuh", "fp4_quant_kernels.cuh", "gemm_fp4_kernel.cuh", "gemm_fp4_pair_kernel.cuh",
-         "splitk_reduce.cuh", "mx4.cuh", "ptx_fp4.cuh"]
+         "splitk_reduce.cuh", "mx4.cuh", "ptx_fp4.cuh", "ptx_load.cuh"]
 
 
 def source(name):
@@ -42,7 +42,7 @@ def test_every_programmatic_kernel_waits_first():
 
 def test_wrappers_are_ordered():
     """The loads' wrappers are volatile and clobber memory."""
-    text = source("ptx.cuh")
+    text = source("ptx_load.cuh")
     found = re.findall(r"asm(.{0,12})\(\s*\"ld\.global[^;]*;\"(.*?)\);", text, flags=re.S)
     assert len(found) >= 3
     for head, tail in found:
